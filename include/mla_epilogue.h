@@ -69,6 +69,9 @@ typedef enum mla_status {
 /* bits the kernel ORs into *status */
 #define MLA_STATUS_SLOT_RANGE 1  /* some slot_mapping[t] >= num_blocks*block_size: that cache row was not written */
 #define MLA_STATUS_POS_RANGE  2  /* some positions[t] outside [0, rope_rows): that token's rows were not rotated */
+#define MLA_STATUS_LEN_RANGE  8  /* mla_latent_gather_launch, mla_prefix_attend_launch: a length, an offset or a position
+                                    outside its block table, or group offsets that do not ascend: cut to what the
+                                    table holds, or the row left out */
 #define MLA_STATUS_TIMEOUT    4  /* a bounded wait inside a kernel (on a copy, a barrier or the tensor cores)
                                     ran out: the outputs are incomplete.  No such wait is expected ever to run
                                     out; the kernel returns instead of hanging */
@@ -197,6 +200,134 @@ typedef struct mla_tuning {
 
 MLA_API void mla_epilogue_set_tuning(const mla_tuning* t);
 MLA_API void mla_epilogue_get_tuning(mla_tuning* out);
+
+/* ======================================================================================
+ * Latent cache rows: writing with a norm and microscaled codes, reading back, attending.
+ *
+ * Formats of a cache row (`format` of the entry points below):
+ *   MLA_CACHE_BF16  576 bf16 values (1152 bytes), as mla_epilogue_launch writes;
+ *   MLA_CACHE_E4M3  576 e4m3 bytes, value = code * *kv_scale, as mla_epilogue_launch
+ *                   writes with MLA_FLAG_KV_FP8;
+ *   MLA_CACHE_MX    656 bytes: 512 e4m3 codes of the latents, then 16 scale bytes, one
+ *                   for each 32 latents (value = code * 2^(byte - 127)), then the 64
+ *                   rotary values in bf16 (at byte 528).
+ * ====================================================================================== */
+#define MLA_CACHE_BF16 0
+#define MLA_CACHE_E4M3 1
+#define MLA_CACHE_MX   2
+
+/*
+ * mla_latent_insert_launch -- one latent cache row per token, with the norm of
+ * the latents, the rotation and the quantisation in the same pass:
+ *
+ *   y  = kv_c[t] * rsqrt(mean(kv_c[t]^2) + eps) * norm_weight   (norm_weight NULL: y = kv_c[t])
+ *   pe = rope(k_pe[t]) with MLA_FLAG_ROPE, else k_pe[t]
+ *   cache.row(slot_mapping[t]) = encode(y || pe)
+ *
+ * y is computed in 64 bits and rounded once to fp32; rope and its table are
+ * those of mla_epilogue_launch (fp32, every operation rounded).  encode:
+ *   MLA_CACHE_BF16  bf16, ties to even;
+ *   MLA_CACHE_E4M3  e4m3 of the IEEE fp32 quotient x / *kv_scale, ties to even,
+ *                   saturating at +-448 (infinities too), NaN stays NaN;
+ *   MLA_CACHE_MX    per 32 latents e = the least integer with max |y| <= 448 * 2^e
+ *                   over the finite y, kept within [-117, 119] (-117 for a group of
+ *                   zeros); code = e4m3 of y * 2^-e as above, scale byte = e + 127;
+ *                   pe in bf16.  Only a value beyond 448 * 2^119 or an infinity
+ *                   saturates; y below 2^-10 * 2^-117 may become zero.
+ *
+ *   kv_c   bf16 [T, 512] at (kv_c_stride_t, 1), 16-byte aligned, stride a multiple of
+ *          8 (unchecked for T == 1); k_pe bf16 [T, 64] at (k_pe_stride_t, 1)
+ *   slot_mapping, positions, cos_sin, rope_rows, kv_scale, status: as in
+ *          mla_epilogue_launch; kv_scale is read with MLA_CACHE_E4M3 only
+ *   norm_weight  bf16 [512], 16-byte aligned, or NULL; eps >= 0 (finite)
+ *   cache  [num_blocks, block_size, row] contiguous, 16-byte aligned
+ *   flags  MLA_FLAG_ROPE, MLA_FLAG_PDL (CONTRACT: the previous kernel on `stream` may
+ *          write kv_c and k_pe only; everything else is read before waiting for it,
+ *          and the cache rows are written after)
+ * T >= 0, T < 2^31.  A token whose slot is negative or out of range writes nothing.
+ */
+MLA_API mla_status mla_latent_insert_launch(
+    const void* kv_c, int64_t kv_c_stride_t,
+    const void* k_pe, int64_t k_pe_stride_t,
+    const int64_t* slot_mapping,
+    const void* norm_weight, float eps,
+    const int32_t* positions, const float* cos_sin, int64_t rope_rows,
+    const float* kv_scale,
+    int64_t T, int64_t block_size, int64_t num_blocks,
+    int32_t format, uint32_t flags,
+    void* cache, int32_t* status, mla_stream_t stream);
+
+/*
+ * mla_latent_gather_launch -- rows of paged sequences read back as bf16:
+ *
+ *   for b < B, cu_rows[b] <= r < cu_rows[b+1], r < N:   k = first[b] + r - cu_rows[b]
+ *     out[r] = bf16(decode(cache.row(block_table[b][k / block_size] * block_size + k % block_size)))
+ *
+ * decode: bf16 rows are copied bit for bit; e4m3 is the fp32 product
+ * code * *kv_scale rounded to bf16; a microscaled value is exact in bf16.
+ *   block_table int32 [B, table_cols] at row stride table_stride (elements)
+ *   cu_rows     int32 [B + 1], ascending; rows r >= cu_rows[B] of out stay as they were
+ *   first       int32 [B] or NULL (0): position each sequence is read from
+ *   out         bf16 [N, 576] at row stride out_stride (a multiple of 8), 16-byte aligned
+ * A page number outside [0, num_blocks) sets MLA_STATUS_SLOT_RANGE, a position
+ * outside the table MLA_STATUS_LEN_RANGE; such a row of out stays as it was.
+ * B >= 0, N >= 0, both < 2^31.  flags: MLA_FLAG_PDL (everything is read after the wait).
+ */
+MLA_API mla_status mla_latent_gather_launch(
+    const void* cache, int32_t format, int64_t block_size, int64_t num_blocks, const float* kv_scale,
+    const int32_t* block_table, int64_t table_stride, int64_t table_cols,
+    const int32_t* cu_rows, const int32_t* first, int64_t B, int64_t N,
+    uint32_t flags, void* out, int64_t out_stride, int32_t* status, mla_stream_t stream);
+
+/*
+ * mla_prefix_attend_launch -- decode attention over the paged latent cache for a
+ * batch whose tokens share long prefixes.  Token t of group g (group_offsets[g] <=
+ * t < group_offsets[g+1]) attends to the prefix_lens[g] keys in the pages
+ * prefix_table[g] and then to its own seq_lens[t] keys in block_table[t]:
+ *
+ *   s[t, h, k]  = sm_scale * sum_d q[t, h, d] * key[k, d]            d < 576
+ *   lse[t, h]   = log sum_k exp(s[t, h, k])
+ *   out[t, h, d] = sum_k exp(s[t, h, k] - lse[t, h]) * key[k, d]     d < 512
+ *
+ * key[k] is the decoded cache row and q the decoded query (e4m3 code * *q_scale
+ * with MLA_FLAG_Q_FP8).  The keys of a prefix are read and multiplied once for
+ * all rows (token, head) of its group, 64 rows at a time.  A row with no keys
+ * gets out = 0 and lse = -inf.  Tokens before group_offsets[0] or from
+ * group_offsets[G] on have no prefix.
+ *
+ * Products run on the tensor cores with fp32 accumulation; scores, softmax
+ * statistics and partial sums are fp32; the softmax weights are rounded to bf16
+ * (to fp16 when both q and the cache are e4m3) before they multiply the keys.
+ *
+ *   q       [T, H, 576] at element strides (q_stride_t, q_stride_h, 1): bf16, or e4m3
+ *           bytes with MLA_FLAG_Q_FP8; 16-byte aligned, strides multiples of 16 bytes
+ *           (unchecked for a size-1 dimension), >= 0
+ *   cache, format, block_size, num_blocks, kv_scale: as above
+ *   prefix_table int32 [G, prefix_cols] at row stride prefix_stride; prefix_lens int32 [G];
+ *           group_offsets int32 [G + 1], ascending (NULL with G == 1: every token).
+ *           G == 0: no prefixes, all three NULL
+ *   block_table int32 [T, table_cols] at row stride table_stride; seq_lens int32 [T].
+ *           table_cols == 0 (block_table NULL): no token has keys of its own
+ *   out     bf16 [T, H, 512] contiguous, 16-byte aligned;  lse fp32 [T, H] or NULL
+ *   workspace  mla_prefix_attend_workspace() bytes of device memory, 256-byte aligned;
+ *           need not be initialised, holds nothing between calls; two calls that may
+ *           run at the same time need two
+ *   flags   MLA_FLAG_Q_FP8, MLA_FLAG_PDL (everything is read after the wait)
+ * A negative length counts as 0.  A length beyond its table is cut to it and sets
+ * MLA_STATUS_LEN_RANGE.  Keys in a page outside [0, num_blocks) are left out and
+ * set MLA_STATUS_SLOT_RANGE.  Keys behind a sequence's length are never read.
+ * T >= 0, 1 <= H <= 65535, T * H < 2^31 - 64, 0 <= G <= T.
+ */
+MLA_API mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int32_t sm_count, int64_t* bytes);
+
+MLA_API mla_status mla_prefix_attend_launch(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const float* q_scale,
+    const void* cache, int32_t format, int64_t block_size, int64_t num_blocks, const float* kv_scale,
+    const int32_t* prefix_table, int64_t prefix_stride, int64_t prefix_cols,
+    const int32_t* prefix_lens, const int32_t* group_offsets, int64_t G,
+    const int32_t* block_table, int64_t table_stride, int64_t table_cols, const int32_t* seq_lens,
+    int64_t T, int64_t H, float sm_scale, uint32_t flags,
+    void* out, float* lse, void* workspace, int64_t workspace_bytes, int32_t* status, mla_stream_t stream);
 
 /* Text for a status code (static storage). */
 MLA_API const char* mla_status_string(mla_status s);

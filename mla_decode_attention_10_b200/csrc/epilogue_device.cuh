@@ -86,16 +86,21 @@ struct Rot {
   bool on;
 };
 
-__device__ __forceinline__ Rot load_rotation(const Args& a, int64_t t, int i) {
+__device__ __forceinline__ Rot load_rotation(const int32_t* positions, const float* cos_sin, int64_t rope_rows,
+                                             int64_t t, int i) {
   Rot r{1.0f, 0.0f, false};
-  const int64_t pos = __ldg(a.positions + t);
-  if (pos >= 0 && pos < a.rope_rows) {
-    const float* row = a.cos_sin + pos * kPe;
+  const int64_t pos = __ldg(positions + t);
+  if (pos >= 0 && pos < rope_rows) {
+    const float* row = cos_sin + pos * kPe;
     r.c = __ldg(row + i);
     r.s = __ldg(row + kHalfPe + i);
     r.on = true;
   }
   return r;
+}
+
+__device__ __forceinline__ Rot load_rotation(const Args& a, int64_t t, int i) {
+  return load_rotation(a.positions, a.cos_sin, a.rope_rows, t, i);
 }
 
 template <bool FP8, bool FAST>

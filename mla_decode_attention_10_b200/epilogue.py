@@ -35,6 +35,11 @@ MLA_FLAG_FORCE_ROWS = 32
 MLA_STATUS_SLOT_RANGE = 1
 MLA_STATUS_POS_RANGE = 2
 MLA_STATUS_TIMEOUT = 4
+MLA_STATUS_LEN_RANGE = 8
+
+MLA_CACHE_BF16 = 0
+MLA_CACHE_E4M3 = 1
+MLA_CACHE_MX = 2
 
 MLA_MODE_SPLIT = 1
 MLA_MODE_ROWS = 2
@@ -44,6 +49,7 @@ MLA_HARNESS_EMPTY_WAIT = 256
 ROW = 576
 NOPE = 512
 PE = 64
+MX_ROW = 656
 
 
 class MlaError(RuntimeError):
@@ -102,6 +108,18 @@ def lib() -> ctypes.CDLL:
         L.mla_absorb_launch.restype = ctypes.c_int
         L.mla_absorb_launch.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i64, i64, u32,
                                         vp, vp, vp]
+        L.mla_latent_insert_launch.restype = ctypes.c_int
+        L.mla_latent_insert_launch.argtypes = [vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, vp, i64, vp,
+                                               i64, i64, i64, i32, u32, vp, vp, vp]
+        L.mla_latent_gather_launch.restype = ctypes.c_int
+        L.mla_latent_gather_launch.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64, i64, u32, vp, i64,
+                                               vp, vp]
+        L.mla_prefix_attend_workspace.restype = ctypes.c_int
+        L.mla_prefix_attend_workspace.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
+        L.mla_prefix_attend_launch.restype = ctypes.c_int
+        L.mla_prefix_attend_launch.argtypes = [vp, i64, i64, vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64,
+                                               vp, i64, i64, vp, i64, i64, ctypes.c_float, u32, vp, vp, vp, i64,
+                                               vp, vp]
         L.mla_harness_div_check.restype = ctypes.c_int
         L.mla_harness_div_check.argtypes = [ctypes.c_float, u64, u64, vp, vp]
         L.mla_harness_bf16_scale_check.restype = ctypes.c_int
@@ -187,6 +205,42 @@ def mla_absorb_launch(q_nope_c, q_nope_c_stride_t, q_nope_c_stride_h, w_uk, q_pe
     return lib().mla_absorb_launch(q_nope_c, q_nope_c_stride_t, q_nope_c_stride_h, w_uk, q_pe, q_pe_stride_t,
                                    q_pe_stride_h, positions, cos_sin, rope_rows, q_scale, T, H, flags, q_out,
                                    status, stream)
+
+
+def mla_latent_insert_launch(kv_c, kv_c_stride_t, k_pe, k_pe_stride_t, slot_mapping, norm_weight, eps, positions,
+                             cos_sin, rope_rows, kv_scale, T, block_size, num_blocks, format, flags, cache, status,
+                             stream) -> int:
+    """Latent cache rows with norm, rotation and quantisation; returns the mla_status code."""
+    return lib().mla_latent_insert_launch(kv_c, kv_c_stride_t, k_pe, k_pe_stride_t, slot_mapping, norm_weight, eps,
+                                          positions, cos_sin, rope_rows, kv_scale, T, block_size, num_blocks, format,
+                                          flags, cache, status, stream)
+
+
+def mla_latent_gather_launch(cache, format, block_size, num_blocks, kv_scale, block_table, table_stride, table_cols,
+                             cu_rows, first, B, N, flags, out, out_stride, status, stream) -> int:
+    """Latent cache rows of paged sequences read back as bf16; returns the mla_status code."""
+    return lib().mla_latent_gather_launch(cache, format, block_size, num_blocks, kv_scale, block_table, table_stride,
+                                          table_cols, cu_rows, first, B, N, flags, out, out_stride, status, stream)
+
+
+def mla_prefix_attend_workspace(T: int, H: int, G: int, sm_count: int = 0) -> int:
+    """Bytes of workspace mla_prefix_attend_launch needs (sm_count 0: of the current device)."""
+    n = ctypes.c_int64()
+    rc = lib().mla_prefix_attend_workspace(T, H, G, sm_count, ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_prefix_attend_workspace")
+    return n.value
+
+
+def mla_prefix_attend_launch(q, q_stride_t, q_stride_h, q_scale, cache, format, block_size, num_blocks, kv_scale,
+                             prefix_table, prefix_stride, prefix_cols, prefix_lens, group_offsets, G, block_table,
+                             table_stride, table_cols, seq_lens, T, H, sm_scale, flags, out, lse, workspace,
+                             workspace_bytes, status, stream) -> int:
+    """Decode attention with shared prefixes over the paged latent cache; returns the mla_status code."""
+    return lib().mla_prefix_attend_launch(q, q_stride_t, q_stride_h, q_scale, cache, format, block_size, num_blocks,
+                                          kv_scale, prefix_table, prefix_stride, prefix_cols, prefix_lens,
+                                          group_offsets, G, block_table, table_stride, table_cols, seq_lens, T, H,
+                                          sm_scale, flags, out, lse, workspace, workspace_bytes, status, stream)
 
 
 # ---- torch convenience ------------------------------------------------------------------
