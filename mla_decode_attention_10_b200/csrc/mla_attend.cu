@@ -69,6 +69,7 @@ constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kWaitSpins = 1u << 22;
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
+constexpr int kSegCost = 2;            // what a segment's start and end cost, in key tiles (see plan_run)
 
 struct Params {
   const uint8_t* q;
@@ -126,7 +127,9 @@ struct Unit {
 
   __device__ __forceinline__ int64_t row_tiles() const { return (rows + kRowsTile - 1) / kRowsTile; }
   __device__ __forceinline__ int64_t key_tiles() const { return (len + kKeys - 1) / kKeys; }
-  __device__ __forceinline__ int64_t tiles() const { return row_tiles() * key_tiles(); }
+  // what one row tile counts for in the deal: kSegCost for its start, then its key tiles
+  __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() + kSegCost : 0; }
+  __device__ __forceinline__ int64_t cost() const { return row_tiles() * row_cost(); }
 };
 
 __device__ __forceinline__ int64_t cut(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
@@ -189,27 +192,29 @@ struct Segment {
 };
 
 struct Cursor {
-  int64_t pos, end;  // tiles of this CTA
-  int64_t base, u;   // first tile of unit u
+  int64_t pos, end;  // this CTA's run
+  int64_t base, u;   // where unit u starts
 };
 
 __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment& s) {
   while (c.pos < c.end) {
     bool bad;
     const Unit x = unit_at(p, c.u, bad);
-    const int64_t kt = x.key_tiles(), n = x.row_tiles() * kt;
+    const int64_t per = x.row_cost(), n = x.row_tiles() * per;
     if (c.pos >= c.base + n) {
       c.base += n;
       ++c.u;
       continue;
     }
-    const int64_t off = c.pos - c.base, r = off / kt, k = off - r * kt;
-    const int64_t take = kt - k < c.end - c.pos ? kt - k : c.end - c.pos;
-    c.pos += take;
+    const int64_t off = c.pos - c.base, r = off / per, from = off - r * per;
+    const int64_t to = per - from < c.end - c.pos ? per : from + (c.end - c.pos);
+    c.pos += to - from;
+    if (to <= kSegCost) continue;  // only the row tile's start: its keys are the next CTA's
+    const int64_t k = from > kSegCost ? from - kSegCost : 0;
     s.row0 = x.rows0 + r * kRowsTile;
     s.rows = static_cast<int32_t>(x.rows - r * kRowsTile < kRowsTile ? x.rows - r * kRowsTile : kRowsTile);
     s.k0 = static_cast<int32_t>(k);
-    s.k1 = static_cast<int32_t>(k + take);
+    s.k1 = static_cast<int32_t>(to - kSegCost);
     s.len = x.len;
     s.table = x.table;
     s.part_rows = x.prefix ? kRowsTile : p.own_rows;
@@ -239,18 +244,41 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(bool f16, int n, bool b
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRowsTile >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One MMA, issued by one lane of the warp.  The warp stays converged, and
+// everything that decides the addresses is uniform over it (broadcast where it
+// comes from memory), so the compiler keeps the descriptors in uniform
+// registers.  Issued from a branch on the lane, each MMA first moved its
+// descriptors there: 50 to 65 cycles, where the N = 64 form takes 32 (the 4 KB
+// of its operands at 128 bytes a cycle).
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "@q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
       : "memory");
 }
 
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
 }
+
+// All MMAs issued so far arrive on the barrier when they have completed.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if (elect_one())
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  __syncwarp();
+}
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -292,40 +320,40 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  for (uint32_t i = 0; i < kWaitSpins; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((i & 15u) == 15u && *abort_flag != 0u) return false;
-  }
-  return false;
-}
-
-// The same for a whole warp: lane 0 polls, and all lanes leave with one answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31u) == 0u) ok = wait_phase(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok) != 0;
-}
-
-// Whether the phase has completed already.
-__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
+// Whether the phase of `parity` has completed.  One lane asks (32 lanes' asking
+// costs 32 times as much of the shared-memory pipe, which the operands and the
+// loaders need), the warp stays converged and gets one answer.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, 0, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  return done != 0;
+  return __any_sync(0xffffffffu, done != 0u) != 0;
+}
+
+// Waits for the phase, at most kWaitSpins tries or until another role gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  for (uint32_t i = 0; i < kWaitSpins; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__any_sync(0xffffffffu, done != 0u)) return true;
+    if ((i & 15u) == 15u && __any_sync(0xffffffffu, *abort_flag != 0u)) return false;
+  }
+  return false;
 }
 
 // barrier `id` over `n` threads, returning the OR of `pred` over them
@@ -355,53 +383,63 @@ __device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// 16 bytes global -> shared without registers; `ok` false writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, o_empty;
+  uint64_t drained;
 };
 
 struct Shared {
   Bars bars;
   uint32_t tmem;
   uint32_t abort_flag;
-  uint32_t valid[kStages][2];  // which keys of a stage's tile count
+  uint32_t never;  // stays 0
+  alignas(16) uint8_t valid[kStages][kKeys];  // 1: the key counts, by stage
   float xch[2][kRowsTile];
   int64_t warp_sum[kThreads / 32];
   int64_t first_unit, first_base;
 };
 
-// ---- the loaders' pieces: thread (row = i / 4, quarter = i % 4) of 64 rows ------
+// ---- the loaders' pieces --------------------------------------------------------
 
-// Raw words of a thread's share of one row, by format.
+// A thread's share of a quantised row (four threads to a row): its words by format.
 template <int FMT>
 struct Raw {
-  static constexpr int kWords = FMT == MLA_CACHE_BF16 ? 18 : FMT == MLA_CACHE_E4M3 ? 9 : 11;
+  static constexpr int kWords = FMT == MLA_CACHE_MX ? 11 : 9;
   uint4 w[kWords];
 };
 
-// A quarter's 16-byte pieces.  16-bit rows: slab s, half i: piece 8 s + 4 (i ^
-// (row & 1)) + quarter (the flip keeps two rows' stores on different banks).
-// e4m3: piece 4 s + quarter.  mx: the same for 8 slabs of codes, then the scale
-// bytes and the quarter's two pieces of rotary values.
+// Word j: e4m3, piece 4 j + quarter.  mx: the same for the 8 slabs of codes, then
+// the scale bytes, then two pieces of rotary values (the flip keeps two rows'
+// stores on different banks).
+template <int FMT>
+__device__ __forceinline__ uint4 load_word(const uint8_t* row, int j, int r, int quarter, bool ok) {
+  const uint4* s = reinterpret_cast<const uint4*>(row);
+  int piece = 4 * j + quarter;
+  if constexpr (FMT == MLA_CACHE_MX) {
+    if (j == 8) piece = kMxScales / 16;
+    if (j > 8) piece = kMxPe / 16 + (((j - 9) ^ (r & 1)) << 2) + quarter;
+  }
+  return ok ? __ldcg(s + piece) : make_uint4(0, 0, 0, 0);
+}
+
 template <int FMT>
 __device__ __forceinline__ void load_row(Raw<FMT>& raw, const uint8_t* row, int r, int quarter, bool ok) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4* s = reinterpret_cast<const uint4*>(row);
-  if constexpr (FMT == MLA_CACHE_BF16) {
 #pragma unroll
-    for (int j = 0; j < 18; ++j) raw.w[j] = ok ? __ldcg(s + (j >> 1) * 8 + (((j & 1) ^ (r & 1)) << 2) + quarter) : zero;
-  } else if constexpr (FMT == MLA_CACHE_E4M3) {
-#pragma unroll
-    for (int j = 0; j < 9; ++j) raw.w[j] = ok ? __ldcg(s + 4 * j + quarter) : zero;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) raw.w[j] = ok ? __ldcg(s + 4 * j + quarter) : zero;
-    raw.w[8] = ok ? __ldcg(s + kMxScales / 16) : zero;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) raw.w[9 + j] = ok ? __ldcg(s + kMxPe / 16 + ((j ^ (r & 1)) << 2) + quarter) : zero;
-  }
+  for (int j = 0; j < Raw<FMT>::kWords; ++j) raw.w[j] = load_word<FMT>(row, j, r, quarter, ok);
 }
 
 // Piece `c` (0..7) of slab `s` of row r in a tile at `base`.
@@ -410,181 +448,399 @@ __device__ __forceinline__ uint32_t piece_addr(uint32_t base, int s, int r, int 
          (static_cast<uint32_t>(c ^ (r & 7)) << 4);
 }
 
+// Word j of a row, decoded, into the tile at `base` (`scales`: word 8 of an mx row).
+template <int FMT, bool F16>
+__device__ __forceinline__ void store_word(const uint4& w, const uint4& scales, int j, uint32_t base, int r, int quarter) {
+  if (FMT == MLA_CACHE_MX && j > 8) {
+    st_shared(piece_addr(base, 8, r, (((j - 9) ^ (r & 1)) << 2) + quarter), w);
+  } else if (FMT == MLA_CACHE_E4M3 || j < 8) {
+    uint4 a, b;
+    if constexpr (FMT == MLA_CACHE_E4M3) {
+      if (any_nan_code(w)) {
+        if constexpr (F16) {
+          codes_to_f16(w, a, b);
+        } else {
+          codes_to_bf16(w, 1.0f, a, b);
+        }
+      } else if constexpr (F16) {
+        plain_codes_to_f16(w, a, b);
+      } else {
+        plain_codes_to_bf16(w, kBf16Pow120, a, b);
+      }
+    } else {
+      // the scale byte of latents 64 j + 16 quarter ..: group 2 j + quarter / 2
+      const uint32_t word = (j >> 1) == 0 ? scales.x : (j >> 1) == 1 ? scales.y : (j >> 1) == 2 ? scales.z : scales.w;
+      const uint32_t byte = (word >> (16 * (j & 1) + 8 * (quarter >> 1))) & 0xffu;
+      if (byte > kMxPlain || any_nan_code(w)) {
+        codes_to_bf16(w, mx_scale(byte), a, b);
+      } else {
+        plain_codes_to_bf16(w, mx_mul2(byte), a, b);
+      }
+    }
+    st_shared(piece_addr(base, j, r, 2 * quarter), a);
+    st_shared(piece_addr(base, j, r, 2 * quarter + 1), b);
+  }
+}
+
 template <int FMT, bool F16>
 __device__ __forceinline__ void store_row(const Raw<FMT>& raw, uint32_t base, int r, int quarter) {
-  if constexpr (FMT == MLA_CACHE_BF16) {
 #pragma unroll
-    for (int j = 0; j < 18; ++j)
-      st_shared(piece_addr(base, j >> 1, r, (((j & 1) ^ (r & 1)) << 2) + quarter), raw.w[j]);
-  } else {
-    constexpr int n = FMT == MLA_CACHE_E4M3 ? 9 : 8;
+  for (int j = 0; j < Raw<FMT>::kWords; ++j)
+    store_word<FMT, F16>(raw.w[j], raw.w[FMT == MLA_CACHE_MX ? 8 : 0], j, base, r, quarter);
+}
+
+// One q row's share of a thread among `LANES` to a row: 16-bit values straight to
+// shared memory, or codes through registers.
+template <int LANES, bool F16>
+__device__ __forceinline__ void load_q16(const uint8_t* row, uint32_t base, int r, int lane, bool ok) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) {
-      uint4 a, b;
-      if constexpr (F16) {
-        codes_to_f16(raw.w[j], a, b);
-      } else if constexpr (FMT == MLA_CACHE_E4M3) {
-        codes_to_bf16(raw.w[j], 1.0f, a, b);
-      } else {
-        // the scale byte of latents 64 j + 16 quarter ..: group 2 j + quarter / 2
-        const uint32_t word = (j >> 1) == 0 ? raw.w[8].x : (j >> 1) == 1 ? raw.w[8].y : (j >> 1) == 2 ? raw.w[8].z : raw.w[8].w;
-        codes_to_bf16(raw.w[j], mx_scale(word >> (16 * (j & 1) + 8 * (quarter >> 1))), a, b);
-      }
-      st_shared(piece_addr(base, j, r, 2 * quarter), a);
-      st_shared(piece_addr(base, j, r, 2 * quarter + 1), b);
-    }
-    if constexpr (FMT == MLA_CACHE_MX) {
+  for (int s = 0; s < kSlabs; ++s) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) st_shared(piece_addr(base, 8, r, ((j ^ (r & 1)) << 2) + quarter), raw.w[9 + j]);
-    }
+    for (int c = 0; c < 8; c += LANES)
+      cp_async16(piece_addr(base, s, r, c + lane), row + (s * 8 + c + lane) * 16, ok);
   }
+}
+
+template <bool F16>
+__device__ __forceinline__ void load_q8(const uint8_t* row, uint32_t base, int r, int quarter, bool ok) {
+  uint4 w[kSlabs];
+#pragma unroll
+  for (int j = 0; j < kSlabs; ++j) w[j] = load_word<MLA_CACHE_E4M3>(row, j, r, quarter, ok);
+#pragma unroll
+  for (int j = 0; j < kSlabs; ++j) store_word<MLA_CACHE_E4M3, F16>(w[j], w[j], j, base, r, quarter);
 }
 
 // ---- the roles ---------------------------------------------------------------------
 
-template <int FMT, bool F16>
-__device__ __forceinline__ void loader(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK) {
-  const int tid = static_cast<int>(threadIdx.x) - 32 * kLoadWarp0;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int r = tid >> 2, quarter = tid & 3;
-  volatile uint32_t* ab = &sh.abort_flag;
-  const uint32_t bs = static_cast<uint32_t>(p.block_size);
-  Segment seg;
-  uint32_t it = 0, nseg = 0;
-  bool bad_page = false, good = true;
-  while (good && next_segment(p, cur, seg)) {
-    // ---- q rows of the segment, once the previous segment's products have read theirs
-    const bool q_ok = r < seg.rows;
-    const int64_t row = seg.row0 + r, t = row / p.H;
-    const uint8_t* src = p.q + t * p.q_st + (row - t * p.H) * p.q_sh;
-    if (p.q_fp8) {
-      Raw<MLA_CACHE_E4M3> raw;
-      load_row<MLA_CACHE_E4M3>(raw, src, r, quarter, q_ok);
-      if (nseg > 0 && !warp_wait(smem_u32(&sh.bars.q_empty), (nseg - 1) & 1u, ab)) good = false;
-      store_row<MLA_CACHE_E4M3, F16>(raw, sQ, r, quarter);
-    } else if constexpr (!F16) {
-      Raw<MLA_CACHE_BF16> raw;
-      load_row<MLA_CACHE_BF16>(raw, src, r, quarter, q_ok);
-      if (nseg > 0 && !warp_wait(smem_u32(&sh.bars.q_empty), (nseg - 1) & 1u, ab)) good = false;
-      store_row<MLA_CACHE_BF16, false>(raw, sQ, r, quarter);
+// A walk over this CTA's key tiles, one at a time.
+struct TileWalk {
+  Cursor cur;
+  const int32_t* table;
+  int32_t len, kt, k1;
+  int32_t row0, rows;  // q rows of the segment
+  int32_t seg;         // segments begun
+  bool first;          // the tile is its segment's first
+
+  __device__ __forceinline__ void start(const Cursor& c) {
+    cur = c;
+    kt = k1 = seg = 0;
+    first = false;
+  }
+  // To the next tile; false behind the last.
+  __device__ __forceinline__ bool next(const Params& p) {
+    first = ++kt >= k1;
+    if (!first) return true;
+    Segment s;
+    if (!next_segment(p, cur, s)) {
+      kt = k1 = 0;
+      return false;
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) arrive(smem_u32(&sh.bars.q_full));
-    ++nseg;
-    // ---- its key tiles
-    for (int kt = seg.k0; good && kt < seg.k1; ++kt, ++it) {
-      const int64_t k = static_cast<int64_t>(kt) * kKeys + r;
-      bool ok = k < seg.len;
-      const uint8_t* krow = p.cache;
-      if (ok) {
-        const uint32_t ku = static_cast<uint32_t>(k);  // lengths are int32
-        const uint32_t pg = ku / bs;
-        const int64_t page = __ldcg(seg.table + pg);
-        if (page < 0 || page >= p.cache_blocks) {
-          ok = false;
-          bad_page = true;
-        } else {
-          krow += (page * p.block_size + (ku - pg * bs)) * row_bytes(FMT);
-        }
-      }
-      Raw<FMT> raw;
-      load_row<FMT>(raw, krow, r, quarter, ok);
-      const uint32_t st = it & 1u;
-      if (it >= kStages && !warp_wait(smem_u32(&sh.bars.kv_empty[st]), (it / kStages - 1) & 1u, ab)) {
-        good = false;
-        break;
-      }
-      store_row<FMT, F16>(raw, sK + st * kTileBytes, r, quarter);
-      const uint32_t b = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) {  // lanes 0, 4, .. 28 stand for the warp's eight rows
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m |= ((b >> (4 * i)) & 1u) << i;
-        reinterpret_cast<volatile uint8_t*>(sh.valid[st])[warp] = static_cast<uint8_t>(m);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(smem_u32(&sh.bars.kv_full[st]));
+    table = s.table;
+    len = static_cast<int32_t>(s.len);
+    kt = s.k0;
+    k1 = s.k1;
+    row0 = static_cast<int32_t>(s.row0);
+    rows = s.rows;
+    ++seg;
+    return true;
+  }
+};
+
+// Where a thread finds the key of its row r in a tile.  The page number is
+// fetched a tile ahead and not looked at before address().
+struct KeyAt {
+  int32_t page;
+  uint32_t in_page;
+  bool key;
+
+  __device__ __forceinline__ void fetch(const Params& p, const TileWalk& w, int r, bool any) {
+    const uint32_t k = static_cast<uint32_t>(w.kt) * kKeys + static_cast<uint32_t>(r);
+    key = any && k < static_cast<uint32_t>(w.len);
+    page = 0;
+    in_page = 0;
+    if (key) {
+      const uint32_t bs = static_cast<uint32_t>(p.block_size), pg = k / bs;
+      in_page = k - pg * bs;
+      page = __ldcg(w.table + pg);
     }
   }
-  if (!good && lane == 0 && *ab == 0u) {
-    *ab = 1u;
+  __device__ __forceinline__ const uint8_t* address(const Params& p, int bytes, bool& ok, bool& bad) const {
+    ok = key && page >= 0 && page < p.cache_blocks;
+    bad = bad || (key && !ok);
+    return ok ? p.cache + (static_cast<int64_t>(page) * p.block_size + in_page) * bytes : p.cache;
+  }
+};
+
+// q row `i` of the `rows` from `row0` on.
+__device__ __forceinline__ const uint8_t* q_row(const Params& p, int32_t row0, int32_t rows, int i, bool& ok) {
+  ok = i < rows;
+  const int32_t row = ok ? row0 + i : 0, t = row / p.H;
+  return p.q + static_cast<int64_t>(t) * p.q_st + static_cast<int64_t>(row - t * p.H) * p.q_sh;
+}
+
+__device__ __forceinline__ void publish(uint32_t bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31u) == 0u) arrive(bar);
+}
+
+// bf16 rows: asynchronous copies straight into the tile, eight threads to a
+// row (whole 128-byte lines), rows r and r + 32 of a thread.  Up to two tiles
+// are under way; a tile is published when its copies have landed, at the
+// latest before this warp waits for a free stage.
+__device__ __forceinline__ bool load_bf16(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
+                                          bool& bad_page) {
+  const int tid = static_cast<int>(threadIdx.x) - 32 * kLoadWarp0;
+  const int r = tid >> 3, c = tid & 7;
+  volatile uint32_t* ab = &sh.abort_flag;
+  TileWalk w;
+  w.start(cur);
+  bool any = w.next(p), good = true;
+  KeyAt at[2];
+  at[0].fetch(p, w, r, any);
+  at[1].fetch(p, w, r + 32, any);
+  uint32_t it = 0, published = 0;
+  bool q_out = false;  // q copies under way with tile it - 1
+  auto publish_tile = [&]() {
+    if (q_out) {
+      publish(smem_u32(&sh.bars.q_full));
+      q_out = false;
+    }
+    publish(smem_u32(&sh.bars.kv_full[published & 1u]));
+    ++published;
+  };
+  while (uniform(any ? 1 : 0) != 0) {
+    const uint32_t st = it & 1u, base = sK + st * kTileBytes;
+    const bool first = uniform(w.first ? 1 : 0) != 0;
+    if (it >= kStages) {
+      const uint32_t bar = smem_u32(&sh.bars.kv_empty[st]), parity = (it / kStages - 1) & 1u;
+      if (published < it && (first || !warp_test(bar, parity))) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (published < it) publish_tile();
+      }
+      if (!warp_wait(bar, parity, ab)) good = false;
+    } else if (first && published < it) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (published < it) publish_tile();
+    }
+    if (first) {  // the segment's q rows, once the previous segment's scores have been computed
+      if (good && w.seg > 1) good = warp_wait(smem_u32(&sh.bars.q_empty), (w.seg - 2) & 1u, ab);
+      if (p.q_fp8) {
+        bool ok;
+        const uint8_t* src = q_row(p, w.row0, w.rows, tid >> 2, ok);
+        load_q8<false>(src, sQ, tid >> 2, tid & 3, ok);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bool ok;
+          const uint8_t* src = q_row(p, w.row0, w.rows, r + 32 * h, ok);
+          load_q16<8, false>(src, sQ, r + 32 * h, c, ok);
+        }
+      }
+      q_out = true;
+    }
+    if (!good) break;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      bool ok;
+      const uint8_t* src = at[h].address(p, row_bytes(MLA_CACHE_BF16), ok, bad_page);
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s) cp_async16(piece_addr(base, s, r + 32 * h, c), src + (s * 8 + c) * 16, ok);
+      if (c == 0) sh.valid[st][r + 32 * h] = ok ? 1 : 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++it;
+    any = w.next(p);
+    at[0].fetch(p, w, r, any);
+    at[1].fetch(p, w, r + 32, any);
+    if (published + 1 < it) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      publish_tile();
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  while (good && published < it) publish_tile();
+  return good;
+}
+
+// Quantised rows: the eight warps form two groups of four, group g has the
+// tiles of stage g.  A tile's rows wait in registers (rows r and r + 32 of a
+// thread, four threads to a row) while the other group's tile is stored, and
+// are decoded on their way to shared memory.
+template <int FMT, bool F16>
+__device__ __forceinline__ bool load_codes(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
+                                           bool& bad_page) {
+  const int tid = (static_cast<int>(threadIdx.x) - 32 * kLoadWarp0) & 127;
+  const uint32_t st = static_cast<uint32_t>(uniform((static_cast<int>(threadIdx.x) - 32 * kLoadWarp0) >> 7));
+  const int r = tid >> 2, quarter = tid & 3;
+  const uint32_t base = sK + st * kTileBytes;
+  volatile uint32_t* ab = &sh.abort_flag;
+  TileWalk w;
+  w.start(cur);
+  bool any = w.next(p);
+  if (st == 1 && any) any = w.next(p);
+  KeyAt at[2];
+  Raw<FMT> raw[2];
+  bool ok[2];
+  auto issue = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* src = at[h].address(p, row_bytes(FMT), ok[h], bad_page);
+      load_row<FMT>(raw[h], src, r + 32 * h, quarter, ok[h]);
+    }
+  };
+  at[0].fetch(p, w, r, any);
+  at[1].fetch(p, w, r + 32, any);
+  issue();
+  for (uint32_t n = 0; uniform(any ? 1 : 0) != 0; ++n) {
+    // what this tile's q rows need; then the walk goes on to this group's next tile
+    const bool first = uniform(w.first ? 1 : 0) != 0;
+    const int32_t row0 = w.row0, rows = w.rows, seg = w.seg;
+    any = w.next(p);
+    if (any) any = w.next(p);
+    at[0].fetch(p, w, r, any);
+    at[1].fetch(p, w, r + 32, any);
+    if (n > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st]), (n - 1) & 1u, ab)) return false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < Raw<FMT>::kWords; ++j)
+        store_word<FMT, F16>(raw[h].w[j], raw[h].w[FMT == MLA_CACHE_MX ? 8 : 0], j, base, r + 32 * h, quarter);
+      if (quarter == 0) sh.valid[st][r + 32 * h] = ok[h] ? 1 : 0;
+    }
+    publish(smem_u32(&sh.bars.kv_full[st]));
+    if (first) {
+      // the segment's q rows, once the previous segment's scores have been computed
+      if (seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab)) return false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bool q_ok;
+        const uint8_t* src = q_row(p, row0, rows, r + 32 * h, q_ok);
+        if (p.q_fp8) {
+          load_q8<F16>(src, sQ, r + 32 * h, quarter, q_ok);
+        } else if constexpr (!F16) {
+          load_q16<4, F16>(src, sQ, r + 32 * h, quarter, q_ok);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      publish(smem_u32(&sh.bars.q_full));
+    }
+    // the next tile's loads go out behind the fences, which would wait for them
+    issue();
+  }
+  return true;
+}
+
+template <int FMT, bool F16>
+__device__ __forceinline__ void loader(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK) {
+  bool bad_page = false, good;
+  if constexpr (FMT == MLA_CACHE_BF16) {
+    good = load_bf16(p, cur, sh, sQ, sK, bad_page);
+  } else {
+    good = load_codes<FMT, F16>(p, cur, sh, sQ, sK, bad_page);
+  }
+  if (!good && (threadIdx.x & 31u) == 0u && sh.abort_flag == 0u) {
+    *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) = 1u;
     report(p.status, MLA_STATUS_TIMEOUT);
   }
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
 }
 
-template <bool F16>
-__device__ __forceinline__ bool issue_pv(Shared& sh, uint32_t sK, uint32_t sP, uint32_t tmem, uint32_t it, bool first,
-                                         uint32_t segs_before, volatile uint32_t* ab) {
-  const uint32_t st = it & 1u;
-  if (!wait_phase(smem_u32(&sh.bars.p_full), it & 1u, ab)) return false;
-  if (first && segs_before > 0 && !wait_phase(smem_u32(&sh.bars.o_empty), (segs_before - 1) & 1u, ab)) return false;
-  fence_after();
+// The products of one tile's weights with its values, into the sums.
+template <bool F16, bool FIRST>
+__device__ __forceinline__ void pv_products(uint64_t p, uint64_t v, uint32_t tmem) {
   constexpr uint32_t id = instr_desc(F16, 256, true);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    const uint32_t d = tmem + static_cast<uint32_t>(half) * 128u;
+    const uint64_t vh = v + static_cast<uint64_t>(half * 4 * (kSlabBytes >> 4));
+    mma_ws<!FIRST>(d, p, vh, id);
 #pragma unroll
-    for (int j = 0; j < kKeys / 16; ++j)
-      mma_ws(tmem + static_cast<uint32_t>(half) * 128u, smem_desc(sP + static_cast<uint32_t>(j) * 32u, 16, 1024),
-             smem_desc(sK + st * kTileBytes + static_cast<uint32_t>(half) * 4u * kSlabBytes + static_cast<uint32_t>(j) * 2048u,
-                       kSlabBytes, 1024),
-             id, (first && j == 0) ? 0u : 1u);
+    for (int j = 1; j < kKeys / 16; ++j)
+      mma_ws<true>(d, p + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j * 128), id);
   }
-  commit(smem_u32(&sh.bars.kv_empty[st]));
-  commit(smem_u32(&sh.bars.pv_done));
-  return true;
 }
 
 template <bool F16>
 __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK, uint32_t sP,
                                          uint32_t tmem) {
   volatile uint32_t* ab = &sh.abort_flag;
-  Segment seg;
-  uint32_t it = 0, nseg = 0;
-  bool good = true;
-  bool prev_first = false;   // whether tile it - 1 is its segment's first
-  uint32_t prev_seg = 0;     // segments before tile it - 1's
-  constexpr uint32_t id = instr_desc(F16, kKeys, false);
-  bool pending = false;      // tile it - 1 has its scores issued, not its sums
-  while (good && next_segment(p, cur, seg)) {
-    // between segments the next scores go first if their operands are there
-    // already; if not, the last tile's sums do not wait for them
-    if (pending && !(test_phase(smem_u32(&sh.bars.q_full), nseg & 1u) &&
-                     test_phase(smem_u32(&sh.bars.kv_full[it & 1u]), (it / kStages) & 1u))) {
-      good = issue_pv<F16>(sh, sK, sP, tmem, it - 1, prev_first, prev_seg, ab);
-      pending = false;
+  const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
+  const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
+  uint32_t s = 0, v = 0;        // the next tile to get scores, and sums: v <= s <= v + 2
+  uint32_t seg = 0;             // segments begun
+  int left = 0;                 // tiles of the current segment without scores
+  bool more = true, first = false;
+  uint32_t first_bits = 0;      // bit (i & 1): tile i is its segment's first
+  uint32_t v_seg = 0;           // segments whose sums have begun
+  uint32_t idle = 0;
+  // whichever has its operands goes: the sums of the oldest tile (they free its
+  // stage), else the scores of the next.  Waiting for a certain one of the two
+  // would let the loaders and the tensor cores wait for each other in turn.
+  while (true) {
+    if (left == 0 && more) {
+      Segment x;
+      left = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
+      more = left > 0;
+      first = true;
+      if (more) ++seg;
     }
-    good = good && wait_phase(smem_u32(&sh.bars.q_full), nseg & 1u, ab);
-    for (int kt = seg.k0; good && kt < seg.k1; ++kt, ++it) {
-      const uint32_t st = it & 1u;
-      good = wait_phase(smem_u32(&sh.bars.kv_full[st]), (it / kStages) & 1u, ab) &&
-             (it < 2 || wait_phase(smem_u32(&sh.bars.s_empty[st]), (it / 2 - 1) & 1u, ab));
-      if (!good) break;
+    if (left == 0 && v == s) break;
+    if (v < s && warp_test(smem_u32(&sh.bars.p_full), v & 1u)) {
+      const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
+      if (!opens || v_seg == 0 || warp_test(smem_u32(&sh.bars.o_empty), (v_seg - 1) & 1u)) {
+        fence_after();
+        const uint64_t vd = dV + (v & 1u) * (kTileBytes >> 4);
+        if (opens) {
+          pv_products<F16, true>(dP, vd, tmem);
+          ++v_seg;
+        } else {
+          pv_products<F16, false>(dP, vd, tmem);
+        }
+        commit(smem_u32(&sh.bars.kv_empty[v & 1u]));
+        commit(smem_u32(&sh.bars.pv_done));
+        ++v;
+        idle = 0;
+        continue;
+      }
+    }
+    const uint32_t st = s & 1u;
+    if (left > 0 && s < v + 2 && warp_test(smem_u32(&sh.bars.kv_full[st]), (s / kStages) & 1u) &&
+        (!first || warp_test(smem_u32(&sh.bars.q_full), (seg - 1) & 1u)) &&
+        (s < 2 || warp_test(smem_u32(&sh.bars.s_empty[st]), (s / 2 - 1) & 1u))) {
       fence_after();
+      constexpr uint32_t id = instr_desc(F16, kKeys, false);
+      const uint64_t k = dK + st * (kTileBytes >> 4);
 #pragma unroll
       for (int j = 0; j < kD / 16; ++j) {
-        const uint32_t off = static_cast<uint32_t>(j >> 2) * kSlabBytes + static_cast<uint32_t>(j & 3) * 32u;
-        mma_ws(tmem + kTmemS + 32u * st, smem_desc(sQ + off, 16, 1024), smem_desc(sK + st * kTileBytes + off, 16, 1024),
-               id, j > 0 ? 1u : 0u);
+        const uint64_t off = static_cast<uint64_t>((j >> 2) * (kSlabBytes >> 4) + (j & 3) * 2);
+        if (j == 0) {
+          mma_ws<false>(tmem + kTmemS + 32u * st, dQ + off, k + off, id);
+        } else {
+          mma_ws<true>(tmem + kTmemS + 32u * st, dQ + off, k + off, id);
+        }
       }
       commit(smem_u32(&sh.bars.s_full[st]));
-      if (kt + 1 == seg.k1) commit(smem_u32(&sh.bars.q_empty));
-      if (pending) good = issue_pv<F16>(sh, sK, sP, tmem, it - 1, prev_first, prev_seg, ab);
-      pending = true;
-      prev_first = kt == seg.k0;
-      prev_seg = nseg;
+      --left;
+      if (left == 0) commit(smem_u32(&sh.bars.q_empty));
+      first_bits = (first_bits & ~(1u << st)) | ((first ? 1u : 0u) << st);
+      first = false;
+      ++s;
+      idle = 0;
+      continue;
     }
-    ++nseg;
+    if (++idle > kWaitSpins || ((idle & 15u) == 15u && __any_sync(0xffffffffu, *ab != 0u))) {
+      if ((threadIdx.x & 31u) == 0u && *ab == 0u) {
+        *ab = 1u;
+        report(p.status, MLA_STATUS_TIMEOUT);
+      }
+      break;
+    }
   }
-  if (good && pending) good = issue_pv<F16>(sh, sK, sP, tmem, it - 1, prev_first, prev_seg, ab);
   // every product issued has completed before TMEM is freed
-  if (good && it > 0) good = wait_phase(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
-  if (!good && *ab == 0u) {
-    *ab = 1u;
-    report(p.status, MLA_STATUS_TIMEOUT);
-  }
+  commit(smem_u32(&sh.bars.drained));
+  (void)warp_wait(smem_u32(&sh.bars.drained), 0u, &sh.never);
 }
 
 template <bool F16>
@@ -612,7 +868,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       fence_after();
       uint32_t v[32];
       tmem_ld32(tmem + kTmemS + 32u * st + lanes, v);
-      const uint32_t valid = *(reinterpret_cast<volatile uint32_t*>(&sh.valid[st][half]));
+      const uint4 va = ld_shared(smem_u32(&sh.valid[st][32 * half])), vb = ld_shared(smem_u32(&sh.valid[st][32 * half + 16]));
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[st]));
@@ -620,9 +876,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]) * scale2;
-      if (valid != 0xffffffffu) {
+      if ((va.x & va.y & va.z & va.w & vb.x & vb.y & vb.z & vb.w) != 0x01010101u) {
+        const uint32_t ok[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = (valid >> j) & 1u ? s[j] : -INFINITY;
+        for (int j = 0; j < 32; ++j) s[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? s[j] : -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < 32; ++j) top = fmaxf(top, s[j]);
@@ -726,7 +983,7 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   bool any_bad = false;
   for (int64_t u = u0; u < u1; ++u) {
     bool bad;
-    sum += unit_at(p, u, bad).tiles();
+    sum += unit_at(p, u, bad).cost();
     any_bad = any_bad || bad;
   }
   if (any_bad && blockIdx.x == 0) report(p.status, MLA_STATUS_LEN_RANGE);
@@ -753,7 +1010,7 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   if (mine || blockIdx.x == 0) {
     for (int64_t u = u0; u < u1; ++u) {
       bool bad;
-      const int64_t n = unit_at(p, u, bad).tiles();
+      const int64_t n = unit_at(p, u, bad).cost();
       if (blockIdx.x == 0) p.plan[1 + u] = base;
       if (c.pos >= base && c.pos < base + n) {
         sh.first_unit = u;
@@ -770,9 +1027,10 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
 
 template <int FMT, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
+  constexpr uint32_t kFillWarps = FMT == MLA_CACHE_BF16 ? kLoadWarps : kLoadWarps / 2;  // that fill one tile
   extern __shared__ uint8_t dsmem[];
   __shared__ Shared sh;
-  const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const int warp = uniform(static_cast<int>(threadIdx.x) >> 5);
   const uint32_t sQ = (smem_u32(dsmem) + 1023u) & ~1023u;
   const uint32_t sK = sQ + kTileBytes;
   const uint32_t sP = sK + kStages * kTileBytes;
@@ -784,22 +1042,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
   }
   if (threadIdx.x == 0) {
     sh.abort_flag = 0u;
+    sh.never = 0u;
     sh.first_unit = 0;
     sh.first_base = 0;
     auto init = [](uint64_t* b, uint32_t n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
     };
     for (int i = 0; i < 2; ++i) {
-      init(&sh.bars.kv_full[i], kLoadWarps);
+      init(&sh.bars.kv_full[i], kFillWarps);
       init(&sh.bars.kv_empty[i], 1);
       init(&sh.bars.s_full[i], 1);
       init(&sh.bars.s_empty[i], kSoftWarps);
     }
-    init(&sh.bars.q_full, kLoadWarps);
+    init(&sh.bars.q_full, kFillWarps);
     init(&sh.bars.q_empty, 1);
     init(&sh.bars.p_full, kSoftWarps);
     init(&sh.bars.pv_done, 1);
     init(&sh.bars.o_empty, kSoftWarps);
+    init(&sh.bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();     // the lengths, q and the cache rows may come from the upstream kernel
@@ -807,16 +1067,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(sh.tmem)));
   const Cursor cur = plan_run(p, sh);
-  if (cur.pos < cur.end) {
+  if (uniform(cur.pos < cur.end ? 1 : 0) != 0) {  // a branch that the compiler sees is uniform
     if (warp < kSoftWarps) {
       float scale2 = p.sm_scale * 1.4426950408889634f;  // powers of two: log2(e)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
       softmax_role<F16>(p, cur, sh, sP, tmem, scale2);
     } else if (warp == kMmaWarp) {
-      if ((threadIdx.x & 31) == 0) mma_role<F16>(p, cur, sh, sQ, sK, sP, tmem);
+      mma_role<F16>(p, cur, sh, sQ, sK, sP, tmem);
     } else {
       loader<FMT, F16>(p, cur, sh, sQ, sK);
     }
@@ -874,20 +1134,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
     bool bad;
     if (g >= 0) {
       const Unit x = unit_at(p, g, bad);
-      const int64_t i = t * p.H + h - x.rows0, kt = x.key_tiles();
-      if (i >= 0 && i < x.rows && kt > 0) {
-        const int64_t tile = i / kRowsTile, f = __ldcg(p.plan + 1 + g) + tile * kt;
-        at1 = f / each + x.part0 + tile;
-        n1 = (f + kt - 1) / each - f / each + 1;
+      const int64_t i = t * p.H + h - x.rows0, per = x.row_cost();
+      if (i >= 0 && i < x.rows && per > 0) {
+        const int64_t tile = i / kRowsTile, f = __ldcg(p.plan + 1 + g) + tile * per;
+        const int64_t c0 = (f + kSegCost) / each;  // the CTA that has the first key tile
+        at1 = c0 + x.part0 + tile;
+        n1 = (f + per - 1) / each - c0 + 1;
         prow = static_cast<int>(i % kRowsTile);
       }
     }
     const Unit x = unit_at(p, p.G + t, bad);
-    const int64_t kt = x.key_tiles(), tile = h / kRowsTile;
-    if (kt > 0) {
-      const int64_t f = __ldcg(p.plan + 1 + p.G + t) + tile * kt;
-      at2 = f / each + x.part0 + tile;
-      n2 = (f + kt - 1) / each - f / each + 1;
+    const int64_t per = x.row_cost(), tile = h / kRowsTile;
+    if (per > 0) {
+      const int64_t f = __ldcg(p.plan + 1 + p.G + t) + tile * per;
+      const int64_t c0 = (f + kSegCost) / each;
+      at2 = c0 + x.part0 + tile;
+      n2 = (f + per - 1) / each - c0 + 1;
     }
   }
   const int n = static_cast<int>(n1 + n2);
@@ -1131,7 +1393,7 @@ mla_status mla_prefix_attend_launch(
 
   const int64_t rows = T * ((H + kJoinRows - 1) / kJoinRows);
   int32_t slices = 1;
-  while (slices < 32 && rows * slices < 2 * sms) slices *= 2;
+  while (slices < 32 && rows * slices < 8 * sms) slices *= 2;
   void* jargs[] = {&p, &slices};
   return launch(reinterpret_cast<const void*>(&join_kernel), rows * slices, kJoinThreads,
                 static_cast<size_t>(2 * sms) * kJoinRows * sizeof(float), true, stream, jargs);

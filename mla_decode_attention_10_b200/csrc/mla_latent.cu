@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256) insert_kernel(const InsertArgs a) {
 }
 
 // ------------------------------------------------------------------------------------
-// gather: a warp per row
+// gather
 // ------------------------------------------------------------------------------------
 
 struct GatherArgs {
@@ -180,6 +180,7 @@ struct GatherArgs {
   int64_t N;
   uint8_t* out;
   int64_t out_stride;  // bytes
+  bool wide;           // rows of out start on 32-byte boundaries
   int32_t* status;
 };
 
@@ -201,63 +202,128 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t B, int
   return lo - 1;
 }
 
+// A warp takes kGatherRows consecutive rows: one search for the first, then lane
+// i < kGatherRows finds row i's sequence, page and address, and every row's
+// loads are issued before any is stored.  (One row per warp, each with its own
+// chain of search, table and row, ran at a third of the copy bandwidth.)
+constexpr int kGatherRows = 8;
+
+// Sixteen values to 32 contiguous bytes.
+__device__ __forceinline__ void store32(uint8_t* dst, bool wide, const uint4& a, const uint4& b) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = a;
+    reinterpret_cast<uint4*>(dst)[1] = b;
+  }
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   pdl_wait();
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (r < a.N) {
-    const int64_t b = sequence_of(a.cu, a.B, r, lane);
-    if (b >= 0) {
-      const int64_t c0 = __ldcg(a.cu + b), c1 = __ldcg(a.cu + b + 1);
-      if (r < c1) {
-        const int64_t k = (a.first != nullptr ? static_cast<int64_t>(__ldcg(a.first + b)) : 0) + r - c0;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kGatherRows;
+  if (r0 < a.N) {
+    // this lane's row: its address, or null
+    const uint8_t* src = nullptr;
+    const int64_t r = r0 + lane;
+    int64_t b = sequence_of(a.cu, a.B, r0, lane);
+    if (lane < kGatherRows && r < a.N) {
+      // on from the first row's sequence to the last one that starts at or before r
+      while (b + 1 < a.B && static_cast<int64_t>(__ldcg(a.cu + b + 1)) <= r) ++b;
+      const int64_t end = b >= 0 ? static_cast<int64_t>(__ldcg(a.cu + b + 1)) : 0;
+      if (b >= 0 && r < end) {
+        const int64_t k = (a.first != nullptr ? static_cast<int64_t>(__ldcg(a.first + b)) : 0) + r - __ldcg(a.cu + b);
         if (k < 0 || k >= a.table_keys) {
-          if (lane == 0) report(a.status, MLA_STATUS_LEN_RANGE);
+          report(a.status, MLA_STATUS_LEN_RANGE);
         } else {
           const int64_t page = __ldcg(a.table + b * a.table_stride + k / a.block_size);
           if (page < 0 || page >= a.cache_blocks) {
-            if (lane == 0) report(a.status, MLA_STATUS_SLOT_RANGE);
+            report(a.status, MLA_STATUS_SLOT_RANGE);
           } else {
-            const uint8_t* src = a.cache + (page * a.block_size + k % a.block_size) * row_bytes(FMT);
-            uint4* dst = reinterpret_cast<uint4*>(a.out + r * a.out_stride);
-            if constexpr (FMT == MLA_CACHE_BF16) {
-              const uint4* s = reinterpret_cast<const uint4*>(src);
-              const uint4 x0 = __ldcg(s + lane), x1 = __ldcg(s + 32 + lane);
-              uint4 x2 = make_uint4(0, 0, 0, 0);
-              if (lane < 8) x2 = __ldcg(s + 64 + lane);
-              dst[lane] = x0;
-              dst[32 + lane] = x1;
-              if (lane < 8) dst[64 + lane] = x2;
-            } else if constexpr (FMT == MLA_CACHE_E4M3) {
-              const uint4* s = reinterpret_cast<const uint4*>(src);
-              const float scale = __ldcg(a.kv_scale);
-              const uint4 c = __ldcg(s + lane);
-              uint4 p = make_uint4(0, 0, 0, 0);
-              if (lane < 4) p = __ldcg(s + 32 + lane);
-              uint4 x, y;
-              codes_to_bf16(c, scale, x, y);
-              dst[2 * lane] = x;
-              dst[2 * lane + 1] = y;
-              if (lane < 4) {
-                codes_to_bf16(p, scale, x, y);
-                dst[64 + 2 * lane] = x;
-                dst[64 + 2 * lane + 1] = y;
-              }
-            } else {
-              const uint4* s = reinterpret_cast<const uint4*>(src);
-              const uint4 c = __ldcg(s + lane);
-              const uint32_t byte = __ldcg(src + kMxScales + (lane >> 1));
-              uint4 p = make_uint4(0, 0, 0, 0);
-              if (lane < 8) p = __ldcg(s + kMxPe / 16 + lane);
-              uint4 x, y;
-              codes_to_bf16(c, mx_scale(byte), x, y);
-              dst[2 * lane] = x;
-              dst[2 * lane + 1] = y;
-              if (lane < 8) dst[64 + lane] = p;
-            }
+            src = a.cache + (page * a.block_size + k % a.block_size) * row_bytes(FMT);
           }
         }
+      }
+    }
+    const uint8_t* rows[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+      rows[i] = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+    uint8_t* out = a.out + r0 * a.out_stride;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if constexpr (FMT == MLA_CACHE_BF16) {
+      // 72 pieces a row: 64 by all lanes, the other 8 of four rows at a time
+#pragma unroll
+      for (int h = 0; h < kGatherRows; h += 4) {
+        uint4 x[8], y = zero;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4* s = reinterpret_cast<const uint4*>(rows[h + i]);
+          if (s != nullptr) {
+            x[2 * i] = __ldcg(s + lane);
+            x[2 * i + 1] = __ldcg(s + 32 + lane);
+          }
+        }
+        const uint4* t = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), h + (lane >> 3)));
+        if (t != nullptr) y = __ldcg(t + 64 + (lane & 7));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (rows[h + i] != nullptr) {
+            uint4* d = reinterpret_cast<uint4*>(out + (h + i) * a.out_stride);
+            d[lane] = x[2 * i];
+            d[32 + lane] = x[2 * i + 1];
+          }
+        }
+        if (t != nullptr) reinterpret_cast<uint4*>(out + (h + (lane >> 3)) * a.out_stride)[64 + (lane & 7)] = y;
+      }
+    } else {
+      uint4 c[kGatherRows];
+      float mul[kGatherRows];
+      float scale = 1.0f;
+      if constexpr (FMT == MLA_CACHE_E4M3) scale = __ldcg(a.kv_scale);
+#pragma unroll
+      for (int i = 0; i < kGatherRows; ++i) {
+        c[i] = zero;
+        uint32_t byte = 127;
+        if (rows[i] != nullptr) {
+          c[i] = __ldcg(reinterpret_cast<const uint4*>(rows[i]) + lane);
+          if constexpr (FMT == MLA_CACHE_MX) byte = __ldcg(rows[i] + kMxScales + (lane >> 1));
+        }
+        mul[i] = FMT == MLA_CACHE_MX ? mx_scale(byte) : scale;
+      }
+      if constexpr (FMT == MLA_CACHE_E4M3) {
+        // the four last pieces of all eight rows
+        const uint8_t* t = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), lane >> 2));
+        uint4 p = zero, x, y;
+        if (t != nullptr) p = __ldcg(reinterpret_cast<const uint4*>(t) + 32 + (lane & 3));
+        codes_to_bf16(p, scale, x, y);
+        if (t != nullptr) store32(out + (lane >> 2) * a.out_stride + 1024 + 32 * (lane & 3), a.wide, x, y);
+      } else {
+        uint4 p[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* t = reinterpret_cast<const uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 4 * h + (lane >> 3)));
+          p[h] = zero;
+          if (t != nullptr) p[h] = __ldcg(reinterpret_cast<const uint4*>(t + kMxPe) + (lane & 7));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 4 * h + (lane >> 3);
+          const bool there = __shfl_sync(0xffffffffu, src != nullptr ? 1 : 0, i) != 0;
+          if (there) reinterpret_cast<uint4*>(out + i * a.out_stride)[64 + (lane & 7)] = p[h];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kGatherRows; ++i) {
+        uint4 x, y;
+        codes_to_bf16(c[i], mul[i], x, y);
+        if (rows[i] != nullptr) store32(out + i * a.out_stride + 32 * lane, a.wide, x, y);
       }
     }
   }
@@ -391,8 +457,12 @@ mla_status mla_latent_gather_launch(const void* cache, int32_t format, int64_t b
   a.N = N;
   a.out = static_cast<uint8_t*>(out);
   a.out_stride = 2 * out_stride;
+  a.wide = aligned(out, 32) && (N == 1 || out_stride % 16 == 0);
   a.status = status;
-  return launch(kGatherKernels[format], (N + 7) / 8, 256, (flags & MLA_FLAG_PDL) != 0, stream, &a);
+  // 8 warps a block; while that leaves SMs without one, one warp a block
+  const int64_t warps = (N + kGatherRows - 1) / kGatherRows;
+  const int per = warps <= sms ? 1 : 8;
+  return launch(kGatherKernels[format], (warps + per - 1) / per, 32 * per, (flags & MLA_FLAG_PDL) != 0, stream, &a);
 }
 
 }  // extern "C"

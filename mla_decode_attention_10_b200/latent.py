@@ -25,65 +25,99 @@ import torch
 
 from . import epilogue as E
 
+# A decode step makes these calls once a layer, so the host side of a call
+# counts: the checks compare integers and interned objects, and a device or
+# stream is only entered when it is not the current one.
 
-def _check(name: str, t: Optional[torch.Tensor], device: torch.device, dtype: torch.dtype, shape: tuple) -> None:
-    """A tensor (if given) of this device, type and shape (None: any size)."""
-    if t is None:
-        return
-    if t.device != device or t.dtype != dtype:
-        raise ValueError(f"{name}: a {dtype} tensor on {device} is required, got {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        want = ", ".join("?" if n is None else str(n) for n in shape)
-        raise ValueError(f"{name}: shape [{want}] is required, got {list(t.shape)}")
+_BF16, _U8, _I32, _I64, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float32
 
 
-def _flat(name: str, t: Optional[torch.Tensor]) -> None:
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _fail(name: str, t: torch.Tensor, index: int, dtype: torch.dtype, shape: tuple) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.get_device() != index or t.dtype != dtype:
+        raise ValueError(f"{name}: a {dtype} tensor on cuda:{index} is required, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {list(shape)} is required, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _inner(name: str, t: torch.Tensor) -> None:
+def _flat(name: str, t: torch.Tensor, index: int, dtype: torch.dtype, shape: tuple) -> int:
+    """The address of a contiguous tensor of this device, type and shape."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        _fail(name, t, index, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor, index: int, dtype: torch.dtype, shape: tuple) -> int:
+    """The address of a tensor of this device, type and shape with inner stride 1."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        _fail(name, t, index, dtype, shape)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: inner stride 1 is required")
+    return t.data_ptr()
 
 
-def _scalar(name: str, t: Optional[torch.Tensor], device: torch.device) -> None:
-    if t is not None and (t.dtype != torch.float32 or t.device != device or t.numel() != 1):
-        raise ValueError(f"{name} must be a one-element fp32 tensor on {device}")
+def _scalar(name: str, t: torch.Tensor, index: int, dtype: torch.dtype) -> int:
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != 1:
+        raise ValueError(f"{name} must be a one-element {dtype} tensor on cuda:{index}")
+    return t.data_ptr()
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _table(name: str, t: torch.Tensor, index: int, rows: int) -> Tuple[int, int, int]:
+    """Address, row stride and columns of an int32 page table of so many rows (-1: any)."""
+    if t.dtype is not _I32 or t.get_device() != index or t.dim() != 2 or (rows >= 0 and t.shape[0] != rows):
+        raise ValueError(f"{name}: an int32 [{'?' if rows < 0 else rows}, pages] tensor on cuda:{index} is required, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: inner stride 1 is required")
+    return t.data_ptr(), t.stride(0), t.shape[1]
 
 
-def _cache_format(cache: torch.Tensor, kv_scale: Optional[torch.Tensor]) -> int:
-    if not cache.is_cuda or cache.dim() != 3 or not cache.is_contiguous():
+def _cache(cache: torch.Tensor, kv_scale: Optional[torch.Tensor]) -> Tuple[int, int, Optional[int]]:
+    """Device index, format and scale address of a cache."""
+    index = cache.get_device()
+    if index < 0 or cache.dim() != 3 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous CUDA tensor [num_blocks, block_size, row]")
-    if cache.dtype == torch.bfloat16 and cache.shape[2] == E.ROW:
-        fmt = E.MLA_CACHE_BF16
-    elif cache.dtype == torch.uint8 and cache.shape[2] == E.ROW:
-        fmt = E.MLA_CACHE_E4M3
-    elif cache.dtype == torch.uint8 and cache.shape[2] == E.MX_ROW:
+    row, dtype = cache.shape[2], cache.dtype
+    if dtype is _U8 and row == E.MX_ROW:
         fmt = E.MLA_CACHE_MX
+    elif dtype is _BF16 and row == E.ROW:
+        fmt = E.MLA_CACHE_BF16
+    elif dtype is _U8 and row == E.ROW:
+        fmt = E.MLA_CACHE_E4M3
     else:
         raise ValueError("cache rows must be 576 bf16, 576 uint8 (e4m3) or 656 uint8 (microscaled)")
     if (kv_scale is not None) != (fmt == E.MLA_CACHE_E4M3):
         raise ValueError("kv_scale belongs to an e4m3 cache ([..., 576] uint8), and to no other")
-    _scalar("kv_scale", kv_scale, cache.device)
-    return fmt
+    return index, fmt, None if kv_scale is None else _scalar("kv_scale", kv_scale, index, _F32)
 
 
-def _status(status: Optional[torch.Tensor], device: torch.device) -> None:
-    if status is not None and (status.dtype != torch.int32 or status.device != device or status.numel() != 1):
-        raise ValueError(f"status must be a one-element int32 tensor on {device}")
-
-
-def _stream(stream: Optional[torch.cuda.Stream], device: torch.device) -> torch.cuda.Stream:
+def _stream(stream: Optional[torch.cuda.Stream], index: int) -> torch.cuda.Stream:
     if stream is None:
-        return torch.cuda.current_stream(device)
-    if stream.device != device:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+        return torch.cuda.current_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
     return stream
+
+
+def _launch(index: int, what: str, entry, *args) -> None:
+    """Calls a C entry point with the tensors' device current."""
+    if torch.cuda.current_device() == index:
+        rc = entry(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = entry(*args)
+    if rc != E.MLA_OK:
+        raise E.MlaError(rc, what)
+
+
+def _empty(shape: tuple, dtype: torch.dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Uninitialised memory that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
 def mla_latent_cache_insert(
@@ -99,33 +133,24 @@ def mla_latent_cache_insert(
     [512]) the latents are RMS-normalised first; with ``cos_sin`` (fp32 [rows,
     64]) and ``positions`` (int32 [T]) the rotary values are rotated.
     """
-    device = cache.device
-    fmt = _cache_format(cache, kv_scale)
+    index, fmt, scale = _cache(cache, kv_scale)
     T = kv_c.shape[0]
-    _check("kv_c", kv_c, device, torch.bfloat16, (T, E.NOPE))
-    _check("k_pe", k_pe, device, torch.bfloat16, (T, E.PE))
-    _check("slot_mapping", slot_mapping, device, torch.int64, (T,))
-    _check("norm_weight", norm_weight, device, torch.bfloat16, (E.NOPE,))
-    _inner("kv_c", kv_c)
-    _inner("k_pe", k_pe)
-    _flat("slot_mapping", slot_mapping)
-    _flat("norm_weight", norm_weight)
-    if (cos_sin is None) != (positions is None):
-        raise ValueError("rotation needs both positions and cos_sin")
-    _check("positions", positions, device, torch.int32, (T,))
-    _check("cos_sin", cos_sin, device, torch.float32, (None, E.PE))
-    _flat("positions", positions)
-    _flat("cos_sin", cos_sin)
-    _status(status, device)
-    flags = (E.MLA_FLAG_ROPE if cos_sin is not None else 0) | (E.MLA_FLAG_PDL if pdl else 0)
-    s = _stream(stream, device)
-    with torch.cuda.device(device):
-        rc = E.mla_latent_insert_launch(
-            _ptr(kv_c), kv_c.stride(0), _ptr(k_pe), k_pe.stride(0), _ptr(slot_mapping), _ptr(norm_weight), eps,
-            _ptr(positions), _ptr(cos_sin), 0 if cos_sin is None else cos_sin.shape[0], _ptr(kv_scale),
-            T, cache.shape[1], cache.shape[0], fmt, flags, _ptr(cache), _ptr(status), s.cuda_stream)
-    if rc != E.MLA_OK:
-        raise E.MlaError(rc, "mla_latent_insert_launch")
+    x = _rows("kv_c", kv_c, index, _BF16, (T, E.NOPE))
+    pe = _rows("k_pe", k_pe, index, _BF16, (T, E.PE))
+    slots = _flat("slot_mapping", slot_mapping, index, _I64, (T,))
+    w = None if norm_weight is None else _flat("norm_weight", norm_weight, index, _BF16, (E.NOPE,))
+    flags, pos, tab, tab_rows = E.MLA_FLAG_PDL if pdl else 0, None, None, 0
+    if cos_sin is not None or positions is not None:
+        if cos_sin is None or positions is None:
+            raise ValueError("rotation needs both positions and cos_sin")
+        tab_rows = cos_sin.shape[0]
+        tab = _flat("cos_sin", cos_sin, index, _F32, (tab_rows, E.PE))
+        pos = _flat("positions", positions, index, _I32, (T,))
+        flags |= E.MLA_FLAG_ROPE
+    st = None if status is None else _scalar("status", status, index, _I32)
+    _launch(index, "mla_latent_insert_launch", E.lib().mla_latent_insert_launch,
+            x, kv_c.stride(0), pe, k_pe.stride(0), slots, w, eps, pos, tab, tab_rows, scale, T, cache.shape[1],
+            cache.shape[0], fmt, flags, cache.data_ptr(), st, _stream(stream, index).cuda_stream)
 
 
 def mla_latent_cache_gather(
@@ -140,40 +165,29 @@ def mla_latent_cache_gather(
     pages], ``cu_rows`` int32 [B + 1], ascending.  Rows of ``out`` that belong
     to no sequence stay as they were (uninitialised in an ``out`` made here).
     """
-    device = cache.device
-    fmt = _cache_format(cache, kv_scale)
-    _check("block_table", block_table, device, torch.int32, (None, None))
-    _inner("block_table", block_table)
+    index, fmt, scale = _cache(cache, kv_scale)
+    table, table_stride, cols = _table("block_table", block_table, index, -1)
     B = block_table.shape[0]
-    _check("cu_rows", cu_rows, device, torch.int32, (B + 1,))
-    _check("first", first, device, torch.int32, (B,))
-    _flat("cu_rows", cu_rows)
-    _flat("first", first)
-    _status(status, device)
-    s = _stream(stream, device)
+    cu = _flat("cu_rows", cu_rows, index, _I32, (B + 1,))
+    at = None if first is None else _flat("first", first, index, _I32, (B,))
+    st = None if status is None else _scalar("status", status, index, _I32)
+    handle = _stream(stream, index).cuda_stream
     if out is None:
-        with torch.cuda.stream(s):
-            out = torch.empty((rows, E.ROW), dtype=torch.bfloat16, device=device)
-    else:
-        _check("out", out, device, torch.bfloat16, (rows, E.ROW))
-        _inner("out", out)
-    with torch.cuda.device(device):
-        rc = E.mla_latent_gather_launch(
-            _ptr(cache), fmt, cache.shape[1], cache.shape[0], _ptr(kv_scale), _ptr(block_table),
-            block_table.stride(0), block_table.shape[1], _ptr(cu_rows), _ptr(first), B, rows,
-            E.MLA_FLAG_PDL if pdl else 0, _ptr(out), out.stride(0), _ptr(status), s.cuda_stream)
-    if rc != E.MLA_OK:
-        raise E.MlaError(rc, "mla_latent_gather_launch")
+        out = _empty((rows, E.ROW), _BF16, index, stream)
+    dst = _rows("out", out, index, _BF16, (rows, E.ROW))
+    _launch(index, "mla_latent_gather_launch", E.lib().mla_latent_gather_launch,
+            cache.data_ptr(), fmt, cache.shape[1], cache.shape[0], scale, table, table_stride, cols, cu, at, B, rows,
+            E.MLA_FLAG_PDL if pdl else 0, dst, out.stride(0), st, handle)
     return out
 
 
 _sm_counts = {}
 
 
-def _sm_count(device: torch.device) -> int:
-    n = _sm_counts.get(device.index)
+def _sm_count(index: int) -> int:
+    n = _sm_counts.get(index)
     if n is None:
-        n = _sm_counts[device.index] = torch.cuda.get_device_properties(device).multi_processor_count
+        n = _sm_counts[index] = torch.cuda.get_device_properties(index).multi_processor_count
     return n
 
 
@@ -199,59 +213,46 @@ def mla_prefix_decode_attention(
     bytes) must not be shared by calls that may run at the same time; without
     one each call takes its own.
     """
-    device = cache.device
-    fmt = _cache_format(cache, kv_scale)
+    index, fmt, scale = _cache(cache, kv_scale)
     if q.dim() != 3:
         raise ValueError("q must be [T, H, 576]")
     T, H = q.shape[0], q.shape[1]
-    _check("q", q, device, torch.bfloat16 if q_scale is None else torch.uint8, (T, H, E.ROW))
-    _inner("q", q)
-    _scalar("q_scale", q_scale, device)
-    if (block_table is None) != (seq_lens is None):
-        raise ValueError("block_table and seq_lens go together")
-    _check("block_table", block_table, device, torch.int32, (T, None))
-    _check("seq_lens", seq_lens, device, torch.int32, (T,))
-    _flat("seq_lens", seq_lens)
-    G = 0
-    if (prefix_table is None) != (prefix_lens is None) or (prefix_table is None and group_offsets is not None):
-        raise ValueError("prefix_table and prefix_lens go together, group_offsets with them")
+    flags = E.MLA_FLAG_PDL if pdl else 0
+    if q_scale is None:
+        qp, qs = _rows("q", q, index, _BF16, (T, H, E.ROW)), None
+    else:
+        qp, qs = _rows("q", q, index, _U8, (T, H, E.ROW)), _scalar("q_scale", q_scale, index, _F32)
+        flags |= E.MLA_FLAG_Q_FP8
+    table, table_stride, cols, lens = None, 0, 0, None
+    if block_table is not None or seq_lens is not None:
+        if block_table is None or seq_lens is None:
+            raise ValueError("block_table and seq_lens go together")
+        table, table_stride, cols = _table("block_table", block_table, index, T)
+        lens = _flat("seq_lens", seq_lens, index, _I32, (T,))
+    G, ptable, pstride, pcols, plens, offsets = 0, None, 0, 0, None, None
     if prefix_table is not None:
+        if prefix_lens is None:
+            raise ValueError("prefix_table and prefix_lens go together")
+        ptable, pstride, pcols = _table("prefix_table", prefix_table, index, -1)
         G = prefix_table.shape[0]
-        _check("prefix_table", prefix_table, device, torch.int32, (None, None))
-        _check("prefix_lens", prefix_lens, device, torch.int32, (G,))
-        _check("group_offsets", group_offsets, device, torch.int32, (G + 1,))
-        _inner("prefix_table", prefix_table)
-        _flat("prefix_lens", prefix_lens)
-        _flat("group_offsets", group_offsets)
-    if block_table is not None:
-        _inner("block_table", block_table)
-    _status(status, device)
-    s = _stream(stream, device)
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        if out is None:
-            out = torch.empty((T, H, E.NOPE), dtype=torch.bfloat16, device=device)
-        else:
-            _check("out", out, device, torch.bfloat16, (T, H, E.NOPE))
-            _flat("out", out)
-        if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=device)
-        else:
-            _check("lse", lse, device, torch.float32, (T, H))
-            _flat("lse", lse)
-        if workspace is None:
-            need = E.mla_prefix_attend_workspace(T, H, G, _sm_count(device))
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            _check("workspace", workspace, device, torch.uint8, (None,))
-            _flat("workspace", workspace)
-        rc = E.mla_prefix_attend_launch(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(q_scale), _ptr(cache), fmt, cache.shape[1], cache.shape[0],
-            _ptr(kv_scale), _ptr(prefix_table), 0 if G == 0 else prefix_table.stride(0),
-            0 if G == 0 else prefix_table.shape[1], _ptr(prefix_lens), _ptr(group_offsets), G,
-            _ptr(block_table), 0 if block_table is None else block_table.stride(0),
-            0 if block_table is None else block_table.shape[1], _ptr(seq_lens), T, H, sm_scale,
-            (E.MLA_FLAG_Q_FP8 if q_scale is not None else 0) | (E.MLA_FLAG_PDL if pdl else 0),
-            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(status), s.cuda_stream)
-    if rc != E.MLA_OK:
-        raise E.MlaError(rc, "mla_prefix_attend_launch")
+        plens = _flat("prefix_lens", prefix_lens, index, _I32, (G,))
+        if group_offsets is not None:
+            offsets = _flat("group_offsets", group_offsets, index, _I32, (G + 1,))
+    elif prefix_lens is not None or group_offsets is not None:
+        raise ValueError("prefix_lens and group_offsets need prefix_table")
+    st = None if status is None else _scalar("status", status, index, _I32)
+    handle = _stream(stream, index).cuda_stream
+    if out is None:
+        out = _empty((T, H, E.NOPE), _BF16, index, stream)
+    if lse is None:
+        lse = _empty((T, H), _F32, index, stream)
+    if workspace is None:
+        workspace = _empty((E.mla_prefix_attend_workspace(T, H, G, _sm_count(index)),), _U8, index, stream)
+    elif workspace.dim() != 1:
+        raise ValueError("workspace must be a one-dimensional uint8 tensor")
+    _launch(index, "mla_prefix_attend_launch", E.lib().mla_prefix_attend_launch,
+            qp, q.stride(0), q.stride(1), qs, cache.data_ptr(), fmt, cache.shape[1], cache.shape[0], scale,
+            ptable, pstride, pcols, plens, offsets, G, table, table_stride, cols, lens, T, H, sm_scale, flags,
+            _flat("out", out, index, _BF16, (T, H, E.NOPE)), _flat("lse", lse, index, _F32, (T, H)),
+            _flat("workspace", workspace, index, _U8, tuple(workspace.shape)), workspace.numel(), st, handle)
     return out, lse
