@@ -309,16 +309,18 @@ MLA_API mla_status mla_latent_gather_launch(
  *   block_table int32 [T, table_cols] at row stride table_stride; seq_lens int32 [T].
  *           table_cols == 0 (block_table NULL): no token has keys of its own
  *   out     bf16 [T, H, 512] contiguous, 16-byte aligned;  lse fp32 [T, H] or NULL
- *   workspace  mla_prefix_attend_workspace() bytes of device memory, 256-byte aligned;
- *           need not be initialised, holds nothing between calls; two calls that may
- *           run at the same time need two
+ *   workspace  mla_prefix_attend_workspace() bytes (prefix_keys = prefix_cols *
+ *           block_size; sm_count 0: of the current device) of device memory,
+ *           256-byte aligned; need not be initialised, holds nothing between calls;
+ *           two calls that may run at the same time need two
  *   flags   MLA_FLAG_Q_FP8, MLA_FLAG_PDL (everything is read after the wait)
  * A negative length counts as 0.  A length beyond its table is cut to it and sets
  * MLA_STATUS_LEN_RANGE.  Keys in a page outside [0, num_blocks) are left out and
  * set MLA_STATUS_SLOT_RANGE.  Keys behind a sequence's length are never read.
  * T >= 0, 1 <= H <= 65535, T * H < 2^31 - 64, 0 <= G <= T.
  */
-MLA_API mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int32_t sm_count, int64_t* bytes);
+MLA_API mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t sm_count,
+                                               int64_t* bytes);
 
 MLA_API mla_status mla_prefix_attend_launch(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, const float* q_scale,

@@ -69,7 +69,11 @@ constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kWaitSpins = 1u << 22;
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
-constexpr int kSegCost = 2;            // what a segment's start and end cost, in key tiles (see plan_run)
+constexpr int kHalfSlabs = 4;          // slabs of a tile's second half; the first half has the rotary slab too
+constexpr uint32_t kImageBytes = kTileBytes + 128;  // a decoded tile as it lies in shared memory, then its 64 flags
+// What the deal counts (measured cycles, in hundreds): a key tile of a decoded
+// prefix, one read from the cache, and a segment's start and end.
+constexpr int kCostImage = 30, kCostRows = 36, kCostCodes = 44, kCostSegment = 70;
 
 struct Params {
   const uint8_t* q;
@@ -91,11 +95,14 @@ struct Params {
   float sm_scale;
   uint16_t* out;
   float* lse;
-  int64_t* plan;      // [0] tiles per CTA, [1 + u] first tile of unit u
+  int64_t* plan;      // [0] each CTA's run, [1 + u] where unit u starts
+  uint8_t* image;     // decoded prefix tiles, or null: prefixes are read from the cache
+  int64_t image_tiles;  // tiles of one group's image
   uint8_t* prefix_part;
   uint8_t* own_part;
   int32_t own_rows;   // rows of an own segment: min(H, 64)
   int32_t ctas;       // CTAs of the attention kernel
+  int32_t tile_cost;  // of a tile read from the cache
   int32_t* status;
 };
 
@@ -122,13 +129,19 @@ struct Unit {
   int64_t rows;
   int64_t len;    // keys
   const int32_t* table;
+  const uint8_t* image;  // its decoded tiles, or null
   bool prefix;
   int64_t part0;  // number of the first row tile, within the unit's kind
 
   __device__ __forceinline__ int64_t row_tiles() const { return (rows + kRowsTile - 1) / kRowsTile; }
   __device__ __forceinline__ int64_t key_tiles() const { return (len + kKeys - 1) / kKeys; }
-  // what one row tile counts for in the deal: kSegCost for its start, then its key tiles
-  __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() + kSegCost : 0; }
+  int32_t tile_cost;
+  // what one row tile counts for in the deal: its start, then its key tiles
+  __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() * tile_cost + kCostSegment : 0; }
+  // the first key tile that starts at or behind position x of the row tile
+  __device__ __forceinline__ int64_t tile_at(int64_t x) const {
+    return x > kCostSegment ? (x - kCostSegment + tile_cost - 1) / tile_cost : 0;
+  }
   __device__ __forceinline__ int64_t cost() const { return row_tiles() * row_cost(); }
 };
 
@@ -162,6 +175,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
     x.rows0 = lo * p.H;
     x.rows = (hi - lo) * p.H;
     x.table = p.prefix_table + u * p.prefix_stride;
+    x.image = p.image != nullptr ? p.image + u * p.image_tiles * kImageBytes : nullptr;
     x.prefix = true;
     x.part0 = x.rows0 / kRowsTile + u;
   } else {
@@ -172,11 +186,13 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
     x.rows0 = t * p.H;
     x.rows = p.H;
     x.table = p.block_table + t * p.table_stride;
+    x.image = nullptr;
     x.prefix = false;
     x.part0 = t * ((p.H + kRowsTile - 1) / kRowsTile);
   }
   bad = bad || len > keys;
   x.len = cut(len, 0, keys);
+  x.tile_cost = x.image != nullptr ? kCostImage : p.tile_cost;
   return x;
 }
 
@@ -187,6 +203,7 @@ struct Segment {
   int32_t k0, k1;
   int64_t len;
   const int32_t* table;
+  const uint8_t* image;
   uint8_t* part;
   int32_t part_rows;
 };
@@ -209,14 +226,16 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
     const int64_t off = c.pos - c.base, r = off / per, from = off - r * per;
     const int64_t to = per - from < c.end - c.pos ? per : from + (c.end - c.pos);
     c.pos += to - from;
-    if (to <= kSegCost) continue;  // only the row tile's start: its keys are the next CTA's
-    const int64_t k = from > kSegCost ? from - kSegCost : 0;
+    // the key tiles that start in this run
+    const int64_t k = x.tile_at(from), k_end = to < per ? x.tile_at(to) : x.key_tiles();
+    if (k >= k_end) continue;
     s.row0 = x.rows0 + r * kRowsTile;
     s.rows = static_cast<int32_t>(x.rows - r * kRowsTile < kRowsTile ? x.rows - r * kRowsTile : kRowsTile);
     s.k0 = static_cast<int32_t>(k);
-    s.k1 = static_cast<int32_t>(to - kSegCost);
+    s.k1 = static_cast<int32_t>(k_end);
     s.len = x.len;
     s.table = x.table;
+    s.image = x.image;
     s.part_rows = x.prefix ? kRowsTile : p.own_rows;
     // segments ascend in (CTA, row tile), so CTA + row tile numbers each one
     s.part = (x.prefix ? p.prefix_part : p.own_part) +
@@ -283,9 +302,11 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void arrive(uint32_t bar, uint32_t count = 1) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // 32 columns of this warp's TMEM lanes, one lane's per thread; the wait names
 // the registers, so no use of them can be scheduled before it.
@@ -394,16 +415,40 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 
+// The barrier gets one arrival of this thread when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// `bytes` contiguous bytes global -> shared by the copy engine, counted on the barrier.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A tile is filled, used and freed in two halves: slabs 0..3 with the rotary
+// slab 8, and slabs 4..7.
 struct Bars {
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t kv_full[kStages][2], kv_empty[kStages][2];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, o_empty;
   uint64_t drained;
 };
 
+struct SegmentInfo {
+  const uint8_t* image;
+  int32_t row0, rows;  // q rows
+};
+
 struct Shared {
   Bars bars;
+  SegmentInfo segments[8];
   uint32_t tmem;
   uint32_t abort_flag;
   uint32_t never;  // stays 0
@@ -414,33 +459,10 @@ struct Shared {
 };
 
 // ---- the loaders' pieces --------------------------------------------------------
-
-// A thread's share of a quantised row (four threads to a row): its words by format.
-template <int FMT>
-struct Raw {
-  static constexpr int kWords = FMT == MLA_CACHE_MX ? 11 : 9;
-  uint4 w[kWords];
-};
-
-// Word j: e4m3, piece 4 j + quarter.  mx: the same for the 8 slabs of codes, then
-// the scale bytes, then two pieces of rotary values (the flip keeps two rows'
-// stores on different banks).
-template <int FMT>
-__device__ __forceinline__ uint4 load_word(const uint8_t* row, int j, int r, int quarter, bool ok) {
-  const uint4* s = reinterpret_cast<const uint4*>(row);
-  int piece = 4 * j + quarter;
-  if constexpr (FMT == MLA_CACHE_MX) {
-    if (j == 8) piece = kMxScales / 16;
-    if (j > 8) piece = kMxPe / 16 + (((j - 9) ^ (r & 1)) << 2) + quarter;
-  }
-  return ok ? __ldcg(s + piece) : make_uint4(0, 0, 0, 0);
-}
-
-template <int FMT>
-__device__ __forceinline__ void load_row(Raw<FMT>& raw, const uint8_t* row, int r, int quarter, bool ok) {
-#pragma unroll
-  for (int j = 0; j < Raw<FMT>::kWords; ++j) raw.w[j] = load_word<FMT>(row, j, r, quarter, ok);
-}
+//
+// A warp has eight rows of a tile.  Its lanes read along the rows (256 or 512
+// contiguous bytes at a time): with a few lanes on each of eight rows the same
+// loads took four times as many passes through the load pipe.
 
 // Piece `c` (0..7) of slab `s` of row r in a tile at `base`.
 __device__ __forceinline__ uint32_t piece_addr(uint32_t base, int s, int r, int c) {
@@ -448,66 +470,95 @@ __device__ __forceinline__ uint32_t piece_addr(uint32_t base, int s, int r, int 
          (static_cast<uint32_t>(c ^ (r & 7)) << 4);
 }
 
-// Word j of a row, decoded, into the tile at `base` (`scales`: word 8 of an mx row).
-template <int FMT, bool F16>
-__device__ __forceinline__ void store_word(const uint4& w, const uint4& scales, int j, uint32_t base, int r, int quarter) {
-  if (FMT == MLA_CACHE_MX && j > 8) {
-    st_shared(piece_addr(base, 8, r, (((j - 9) ^ (r & 1)) << 2) + quarter), w);
-  } else if (FMT == MLA_CACHE_E4M3 || j < 8) {
-    uint4 a, b;
-    if constexpr (FMT == MLA_CACHE_E4M3) {
-      if (any_nan_code(w)) {
-        if constexpr (F16) {
-          codes_to_f16(w, a, b);
-        } else {
-          codes_to_bf16(w, 1.0f, a, b);
-        }
-      } else if constexpr (F16) {
-        plain_codes_to_f16(w, a, b);
-      } else {
-        plain_codes_to_bf16(w, kBf16Pow120, a, b);
-      }
-    } else {
-      // the scale byte of latents 64 j + 16 quarter ..: group 2 j + quarter / 2
-      const uint32_t word = (j >> 1) == 0 ? scales.x : (j >> 1) == 1 ? scales.y : (j >> 1) == 2 ? scales.z : scales.w;
-      const uint32_t byte = (word >> (16 * (j & 1) + 8 * (quarter >> 1))) & 0xffu;
-      if (byte > kMxPlain || any_nan_code(w)) {
-        codes_to_bf16(w, mx_scale(byte), a, b);
-      } else {
-        plain_codes_to_bf16(w, mx_mul2(byte), a, b);
-      }
+// What a lane holds of its warp's eight quantised rows.  Half h of rows 2 j and
+// 2 j + 1 (lanes 0..15 and 16..31): codes[4 h + j], 16 codes a lane.  The rest
+// of the rows: the rotary values.
+template <int FMT>
+struct Raw {
+  uint4 codes[8];
+  uint4 rest[FMT == MLA_CACHE_MX ? 2 : 1];
+  uint4 scales;  // mx: the 16 scale bytes of row `lane` (lanes 0..7)
+};
+
+// The address of row i of the warp's eight from the lane that holds it; null: no key.
+__device__ __forceinline__ const uint8_t* row_at(const uint8_t* mine, int i) {
+  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
+}
+
+template <int FMT>
+__device__ __forceinline__ void load_rows(Raw<FMT>& raw, const uint8_t* mine, int lane) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint8_t* row = row_at(mine, 2 * j + (lane >> 4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      raw.codes[4 * h + j] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row) + 16 * h + (lane & 15)) : zero;
     }
-    st_shared(piece_addr(base, j, r, 2 * quarter), a);
-    st_shared(piece_addr(base, j, r, 2 * quarter + 1), b);
+  }
+  if constexpr (FMT == MLA_CACHE_MX) {
+    raw.scales = mine != nullptr ? __ldcg(reinterpret_cast<const uint4*>(mine + kMxScales)) : zero;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* row = row_at(mine, 4 * i + (lane >> 3));
+      raw.rest[i] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row + kMxPe) + (lane & 7)) : zero;
+    }
+  } else {
+    const uint8_t* row = row_at(mine, lane >> 2);
+    raw.rest[0] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row) + 32 + (lane & 3)) : zero;
   }
 }
 
+// Sixteen codes -> two pieces of 16-bit values.
 template <int FMT, bool F16>
-__device__ __forceinline__ void store_row(const Raw<FMT>& raw, uint32_t base, int r, int quarter) {
-#pragma unroll
-  for (int j = 0; j < Raw<FMT>::kWords; ++j)
-    store_word<FMT, F16>(raw.w[j], raw.w[FMT == MLA_CACHE_MX ? 8 : 0], j, base, r, quarter);
-}
-
-// One q row's share of a thread among `LANES` to a row: 16-bit values straight to
-// shared memory, or codes through registers.
-template <int LANES, bool F16>
-__device__ __forceinline__ void load_q16(const uint8_t* row, uint32_t base, int r, int lane, bool ok) {
-#pragma unroll
-  for (int s = 0; s < kSlabs; ++s) {
-#pragma unroll
-    for (int c = 0; c < 8; c += LANES)
-      cp_async16(piece_addr(base, s, r, c + lane), row + (s * 8 + c + lane) * 16, ok);
+__device__ __forceinline__ void decode(const uint4& w, uint32_t byte, uint4& a, uint4& b) {
+  if constexpr (F16) {
+    if (any_nan_code(w)) {
+      codes_to_f16(w, a, b);
+    } else {
+      plain_codes_to_f16(w, a, b);
+    }
+  } else {
+    if ((FMT == MLA_CACHE_MX && byte > kMxPlain) || any_nan_code(w)) {
+      codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_scale(byte) : 1.0f, a, b);
+    } else {
+      plain_codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_mul2(byte) : kBf16Pow120, a, b);
+    }
   }
 }
 
-template <bool F16>
-__device__ __forceinline__ void load_q8(const uint8_t* row, uint32_t base, int r, int quarter, bool ok) {
-  uint4 w[kSlabs];
+// Half h of the warp's rows, decoded, through `put(slab, row, piece, value)`.
+// A lane's two pieces swap places in odd slabs, so that eight lanes' stores
+// fall on different banks.
+template <int FMT, bool F16, class Put>
+__device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0, int lane, const Put& put) {
+  const int slab = 4 * h + ((lane & 15) >> 2), piece = 2 * (lane & 3), odd = (lane >> 2) & 1;
 #pragma unroll
-  for (int j = 0; j < kSlabs; ++j) w[j] = load_word<MLA_CACHE_E4M3>(row, j, r, quarter, ok);
+  for (int j = 0; j < 4; ++j) {
+    const int r = row0 + 2 * j + (lane >> 4);
+    uint32_t byte = 0;
+    if constexpr (FMT == MLA_CACHE_MX) {  // of group 8 h + (lane & 15) / 2
+      const int from = 2 * j + (lane >> 4);
+      const uint32_t lo = __shfl_sync(0xffffffffu, h == 0 ? raw.scales.x : raw.scales.z, from);
+      const uint32_t hi = __shfl_sync(0xffffffffu, h == 0 ? raw.scales.y : raw.scales.w, from);
+      byte = (((lane & 8) != 0 ? hi : lo) >> (8 * ((lane >> 1) & 3))) & 0xffu;
+    }
+    uint4 a, b;
+    decode<FMT, F16>(raw.codes[4 * h + j], byte, a, b);
+    put(slab, r, piece + odd, odd ? b : a);
+    put(slab, r, piece + (odd ^ 1), odd ? a : b);
+  }
+  if (h == 0) {
+    if constexpr (FMT == MLA_CACHE_MX) {
 #pragma unroll
-  for (int j = 0; j < kSlabs; ++j) store_word<MLA_CACHE_E4M3, F16>(w[j], w[j], j, base, r, quarter);
+      for (int i = 0; i < 2; ++i) put(8, row0 + 4 * i + (lane >> 3), lane & 7, raw.rest[i]);
+    } else {
+      uint4 a, b;
+      decode<FMT, F16>(raw.rest[0], 0u, a, b);
+      put(8, row0 + (lane >> 2), 2 * (lane & 3), a);
+      put(8, row0 + (lane >> 2), 2 * (lane & 3) + 1, b);
+    }
+  }
 }
 
 // ---- the roles ---------------------------------------------------------------------
@@ -517,57 +568,71 @@ struct TileWalk {
   Cursor cur;
   const int32_t* table;
   int32_t len, kt, k1;
-  int32_t row0, rows;  // q rows of the segment
-  int32_t seg;         // segments begun
-  bool first;          // the tile is its segment's first
+  int32_t seg;   // segments begun
+  bool copied;   // the segment's tiles come from an image
+  bool first;    // the tile is its segment's first
+  bool any;      // not yet behind the last
 
   __device__ __forceinline__ void start(const Cursor& c) {
     cur = c;
     kt = k1 = seg = 0;
-    first = false;
+    copied = first = false;
+    any = true;
   }
-  // To the next tile; false behind the last.
-  __device__ __forceinline__ bool next(const Params& p) {
+  // To the next tile.
+  __device__ __forceinline__ void next(const Params& p, Shared& sh) {
+    if (!any) return;
     first = ++kt >= k1;
-    if (!first) return true;
+    if (!first) return;
     Segment s;
-    if (!next_segment(p, cur, s)) {
-      kt = k1 = 0;
-      return false;
-    }
+    any = next_segment(p, cur, s);
+    if (!any) return;
     table = s.table;
     len = static_cast<int32_t>(s.len);
     kt = s.k0;
     k1 = s.k1;
-    row0 = static_cast<int32_t>(s.row0);
-    rows = s.rows;
+    copied = s.image != nullptr;
     ++seg;
-    return true;
+    // Kept for the tiles' own turn.  Every loader warp writes the same values;
+    // they are at most 2 + 2 + 1 segments apart, so none is overwritten too early.
+    volatile SegmentInfo& i = sh.segments[seg & 7];
+    i.image = s.image;
+    i.row0 = static_cast<int32_t>(s.row0);
+    i.rows = s.rows;
   }
 };
 
-// Where a thread finds the key of its row r in a tile.  The page number is
-// fetched a tile ahead and not looked at before address().
+struct Tile {
+  int32_t kt, seg;
+  bool copied, first, any;
+
+  __device__ __forceinline__ explicit Tile(const TileWalk& w)
+      : kt(w.kt), seg(w.seg), copied(w.copied), first(w.first), any(w.any) {}
+};
+
+// Where the key of row r of a tile lies.  The page number is fetched a tile
+// ahead and not looked at before address().
 struct KeyAt {
   int32_t page;
   uint32_t in_page;
   bool key;
 
-  __device__ __forceinline__ void fetch(const Params& p, const TileWalk& w, int r, bool any) {
-    const uint32_t k = static_cast<uint32_t>(w.kt) * kKeys + static_cast<uint32_t>(r);
-    key = any && k < static_cast<uint32_t>(w.len);
+  __device__ __forceinline__ void fetch(const Params& p, const int32_t* table, int32_t len, int32_t kt, int r, bool any) {
+    const uint32_t k = static_cast<uint32_t>(kt) * kKeys + static_cast<uint32_t>(r);
+    key = any && k < static_cast<uint32_t>(len);
     page = 0;
     in_page = 0;
     if (key) {
       const uint32_t bs = static_cast<uint32_t>(p.block_size), pg = k / bs;
       in_page = k - pg * bs;
-      page = __ldcg(w.table + pg);
+      page = __ldcg(table + pg);
     }
   }
-  __device__ __forceinline__ const uint8_t* address(const Params& p, int bytes, bool& ok, bool& bad) const {
-    ok = key && page >= 0 && page < p.cache_blocks;
+  // null: no key, or no such page (`bad`)
+  __device__ __forceinline__ const uint8_t* address(const Params& p, int bytes, bool& bad) const {
+    const bool ok = key && page >= 0 && page < p.cache_blocks;
     bad = bad || (key && !ok);
-    return ok ? p.cache + (static_cast<int64_t>(page) * p.block_size + in_page) * bytes : p.cache;
+    return ok ? p.cache + (static_cast<int64_t>(page) * p.block_size + in_page) * bytes : nullptr;
   }
 };
 
@@ -578,187 +643,212 @@ __device__ __forceinline__ const uint8_t* q_row(const Params& p, int32_t row0, i
   return p.q + static_cast<int64_t>(t) * p.q_st + static_cast<int64_t>(row - t * p.H) * p.q_sh;
 }
 
-__device__ __forceinline__ void publish(uint32_t bar) {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
-  if ((threadIdx.x & 31u) == 0u) arrive(bar);
+// The segment's 64 q rows, by all loader threads; q_full gets one arrival of each.
+template <bool F16>
+__device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t rows, uint32_t sQ, uint32_t bar, int warp,
+                                       int lane) {
+  bool ok;
+  if (p.q_fp8) {
+    const uint8_t* src = q_row(p, row0, rows, 8 * warp + (lane & 7), ok);
+    Raw<MLA_CACHE_E4M3> raw;
+    load_rows<MLA_CACHE_E4M3>(raw, ok && lane < 8 ? src : nullptr, lane);
+    auto put = [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(sQ, s, r, c), v); };
+    store_half<MLA_CACHE_E4M3, F16>(raw, 0, 8 * warp, lane, put);
+    store_half<MLA_CACHE_E4M3, F16>(raw, 1, 8 * warp, lane, put);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) arrive(bar, 32);
+  } else if constexpr (!F16) {
+    // eight lanes to a row: rows 8 warp + lane / 8 and four further on
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * warp + 4 * i + (lane >> 3);
+      const uint8_t* src = q_row(p, row0, rows, r, ok);
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s) cp_async16(piece_addr(sQ, s, r, lane & 7), src + (s * 8 + (lane & 7)) * 16, ok);
+    }
+    cp_async_arrive(bar);
+  }
 }
 
-// bf16 rows: asynchronous copies straight into the tile, eight threads to a
-// row (whole 128-byte lines), rows r and r + 32 of a thread.  Up to two tiles
-// are under way; a tile is published when its copies have landed, at the
-// latest before this warp waits for a free stage.
-__device__ __forceinline__ bool load_bf16(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
-                                          bool& bad_page) {
-  const int tid = static_cast<int>(threadIdx.x) - 32 * kLoadWarp0;
-  const int r = tid >> 3, c = tid & 7;
+// Loader warps fill the stages, tile by tile.  kArrive: what one warp's part of
+// a half counts on its barrier.
+template <int FMT, bool F16>
+__device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
+                                           bool& bad_page) {
+  constexpr bool kCodes = FMT != MLA_CACHE_BF16;
+  constexpr uint32_t kArrive = kCodes ? 1 : 33;
+  const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - kLoadWarp0), lane = static_cast<int>(threadIdx.x) & 31;
+  const int row0 = 8 * warp;
   volatile uint32_t* ab = &sh.abort_flag;
-  TileWalk w;
-  w.start(cur);
-  bool any = w.next(p), good = true;
-  KeyAt at[2];
-  at[0].fetch(p, w, r, any);
-  at[1].fetch(p, w, r + 32, any);
-  uint32_t it = 0, published = 0;
-  bool q_out = false;  // q copies under way with tile it - 1
-  auto publish_tile = [&]() {
-    if (q_out) {
-      publish(smem_u32(&sh.bars.q_full));
-      q_out = false;
-    }
-    publish(smem_u32(&sh.bars.kv_full[published & 1u]));
-    ++published;
+  // Lane i < 8 looks after row i of the warp's eight: its page number is fetched
+  // two tiles ahead, its row called to L2 one and a half ahead.
+  TileWalk w;  // two tiles ahead of the one being stored
+  KeyAt at;
+  Raw<kCodes ? FMT : MLA_CACHE_E4M3> raw;
+  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, row0 + lane, w.any && lane < 8 && !w.copied); };
+  auto call = [&](const uint8_t* row) {
+    if (row != nullptr)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "n"(row_bytes(FMT)) : "memory");
   };
-  while (uniform(any ? 1 : 0) != 0) {
-    const uint32_t st = it & 1u, base = sK + st * kTileBytes;
-    const bool first = uniform(w.first ? 1 : 0) != 0;
-    if (it >= kStages) {
-      const uint32_t bar = smem_u32(&sh.bars.kv_empty[st]), parity = (it / kStages - 1) & 1u;
-      if (published < it && (first || !warp_test(bar, parity))) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        while (published < it) publish_tile();
-      }
-      if (!warp_wait(bar, parity, ab)) good = false;
-    } else if (first && published < it) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      while (published < it) publish_tile();
-    }
-    if (first) {  // the segment's q rows, once the previous segment's scores have been computed
-      if (good && w.seg > 1) good = warp_wait(smem_u32(&sh.bars.q_empty), (w.seg - 2) & 1u, ab);
-      if (p.q_fp8) {
-        bool ok;
-        const uint8_t* src = q_row(p, w.row0, w.rows, tid >> 2, ok);
-        load_q8<false>(src, sQ, tid >> 2, tid & 3, ok);
+  w.start(cur);
+  w.next(p, sh);
+  Tile now(w);
+  fetch();
+  const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
+  w.next(p, sh);
+  Tile then(w);
+  fetch();
+  const uint8_t* next_row = at.address(p, row_bytes(FMT), bad_page);
+  call(next_row);
+  w.next(p, sh);
+  fetch();
+  if constexpr (kCodes) load_rows<FMT>(raw, mine, lane);
+  for (uint32_t it = 0; uniform(now.any ? 1 : 0) != 0; ++it) {
+    const uint32_t st = it & 1u, base = sK + st * kTileBytes, parity = (it / kStages - 1) & 1u;
+    const uint32_t full0 = smem_u32(&sh.bars.kv_full[st][0]), full1 = smem_u32(&sh.bars.kv_full[st][1]);
+    const bool direct = uniform(now.copied ? 0 : 1) != 0;
+    const bool first = uniform(now.first ? 1 : 0) != 0;
+    const volatile SegmentInfo& info = sh.segments[now.seg & 7];
+    const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * kImageBytes;
+    const bool ok = mine != nullptr;
+    // ---- first half
+    if (it >= kStages && !warp_wait(smem_u32(&sh.bars.kv_empty[st][0]), parity, ab)) return false;
+    if (direct) {
+      if (lane < 8) sh.valid[st][row0 + lane] = ok ? 1 : 0;
+      if constexpr (kCodes) {
+        store_half<FMT, F16>(raw, 0, row0, lane,
+                             [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
+        fence_async();
+        __syncwarp();
+        if (lane == 0) arrive(full0);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          bool ok;
-          const uint8_t* src = q_row(p, w.row0, w.rows, r + 32 * h, ok);
-          load_q16<8, false>(src, sQ, r + 32 * h, c, ok);
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* src = row_at(mine, i);
+          cp_async16(piece_addr(base, lane >> 3, row0 + i, lane & 7), (src != nullptr ? src : p.cache) + 16 * lane, src != nullptr);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const uint8_t* src = row_at(mine, r);
+          cp_async16(piece_addr(base, 8, row0 + r, lane & 7), (src != nullptr ? src : p.cache) + 1024 + 16 * (lane & 7), src != nullptr);
+        }
+        cp_async_arrive(full0);
+        __syncwarp();
+        if (lane == 0) arrive(full0);
       }
-      q_out = true;
+    } else if (warp == 0) {
+      if (elect_one()) {
+        if (kArrive > 1) arrive(full0, kArrive - 1);
+        arrive_expect(full0, 5 * kSlabBytes + kKeys);
+        bulk_copy(base, image, 4 * kSlabBytes, full0);
+        bulk_copy(base + 8 * kSlabBytes, image + 8 * kSlabBytes, kSlabBytes, full0);
+        bulk_copy(smem_u32(sh.valid[st]), image + kTileBytes, kKeys, full0);
+      }
+      __syncwarp();
+    } else {
+      if (lane == 0) arrive(full0, kArrive);
     }
-    if (!good) break;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bool ok;
-      const uint8_t* src = at[h].address(p, row_bytes(MLA_CACHE_BF16), ok, bad_page);
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s) cp_async16(piece_addr(base, s, r + 32 * h, c), src + (s * 8 + c) * 16, ok);
-      if (c == 0) sh.valid[st][r + 32 * h] = ok ? 1 : 0;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    ++it;
-    any = w.next(p);
-    at[0].fetch(p, w, r, any);
-    at[1].fetch(p, w, r + 32, any);
-    if (published + 1 < it) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      publish_tile();
-    }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  while (good && published < it) publish_tile();
-  return good;
-}
-
-// Quantised rows: the eight warps form two groups of four, group g has the
-// tiles of stage g.  A tile's rows wait in registers (rows r and r + 32 of a
-// thread, four threads to a row) while the other group's tile is stored, and
-// are decoded on their way to shared memory.
-template <int FMT, bool F16>
-__device__ __forceinline__ bool load_codes(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
-                                           bool& bad_page) {
-  const int tid = (static_cast<int>(threadIdx.x) - 32 * kLoadWarp0) & 127;
-  const uint32_t st = static_cast<uint32_t>(uniform((static_cast<int>(threadIdx.x) - 32 * kLoadWarp0) >> 7));
-  const int r = tid >> 2, quarter = tid & 3;
-  const uint32_t base = sK + st * kTileBytes;
-  volatile uint32_t* ab = &sh.abort_flag;
-  TileWalk w;
-  w.start(cur);
-  bool any = w.next(p);
-  if (st == 1 && any) any = w.next(p);
-  KeyAt at[2];
-  Raw<FMT> raw[2];
-  bool ok[2];
-  auto issue = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* src = at[h].address(p, row_bytes(FMT), ok[h], bad_page);
-      load_row<FMT>(raw[h], src, r + 32 * h, quarter, ok[h]);
-    }
-  };
-  at[0].fetch(p, w, r, any);
-  at[1].fetch(p, w, r + 32, any);
-  issue();
-  for (uint32_t n = 0; uniform(any ? 1 : 0) != 0; ++n) {
-    // what this tile's q rows need; then the walk goes on to this group's next tile
-    const bool first = uniform(w.first ? 1 : 0) != 0;
-    const int32_t row0 = w.row0, rows = w.rows, seg = w.seg;
-    any = w.next(p);
-    if (any) any = w.next(p);
-    at[0].fetch(p, w, r, any);
-    at[1].fetch(p, w, r + 32, any);
-    if (n > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st]), (n - 1) & 1u, ab)) return false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < Raw<FMT>::kWords; ++j)
-        store_word<FMT, F16>(raw[h].w[j], raw[h].w[FMT == MLA_CACHE_MX ? 8 : 0], j, base, r + 32 * h, quarter);
-      if (quarter == 0) sh.valid[st][r + 32 * h] = ok[h] ? 1 : 0;
-    }
-    publish(smem_u32(&sh.bars.kv_full[st]));
     if (first) {
       // the segment's q rows, once the previous segment's scores have been computed
-      if (seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab)) return false;
+      if (now.seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
+      load_q<F16>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
+    }
+    // ---- second half
+    if (it >= kStages && !warp_wait(smem_u32(&sh.bars.kv_empty[st][1]), parity, ab)) return false;
+    if (direct) {
+      if constexpr (kCodes) {
+        store_half<FMT, F16>(raw, 1, row0, lane,
+                             [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
+        fence_async();
+        __syncwarp();
+        if (lane == 0) arrive(full1);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        bool q_ok;
-        const uint8_t* src = q_row(p, row0, rows, r + 32 * h, q_ok);
-        if (p.q_fp8) {
-          load_q8<F16>(src, sQ, r + 32 * h, quarter, q_ok);
-        } else if constexpr (!F16) {
-          load_q16<4, F16>(src, sQ, r + 32 * h, quarter, q_ok);
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* src = row_at(mine, i);
+          cp_async16(piece_addr(base, 4 + (lane >> 3), row0 + i, lane & 7), (src != nullptr ? src : p.cache) + 512 + 16 * lane, src != nullptr);
         }
+        cp_async_arrive(full1);
+        __syncwarp();
+        if (lane == 0) arrive(full1);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      publish(smem_u32(&sh.bars.q_full));
+    } else if (warp == 0) {
+      if (elect_one()) {
+        if (kArrive > 1) arrive(full1, kArrive - 1);
+        arrive_expect(full1, 4 * kSlabBytes);
+        bulk_copy(base + 4 * kSlabBytes, image + 4 * kSlabBytes, 4 * kSlabBytes, full1);
+      }
+      __syncwarp();
+    } else {
+      if (lane == 0) arrive(full1, kArrive);
     }
     // the next tile's loads go out behind the fences, which would wait for them
-    issue();
+    mine = next_row;
+    if constexpr (kCodes) load_rows<FMT>(raw, mine, lane);
+    next_row = at.address(p, row_bytes(FMT), bad_page);
+    call(next_row);
+    now = then;
+    then = Tile(w);
+    w.next(p, sh);
+    fetch();
   }
   return true;
 }
 
 template <int FMT, bool F16>
 __device__ __forceinline__ void loader(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK) {
-  bool bad_page = false, good;
-  if constexpr (FMT == MLA_CACHE_BF16) {
-    good = load_bf16(p, cur, sh, sQ, sK, bad_page);
-  } else {
-    good = load_codes<FMT, F16>(p, cur, sh, sQ, sK, bad_page);
+  bool bad_page = false;
+  const bool good = load_tiles<FMT, F16>(p, cur, sh, sQ, sK, bad_page);
+  // no copy may be under way when the CTA ends: on the way out after a timeout
+  // (else every copy's tile has been used) give the copy engine's theirs
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!good) {
+    for (int i = 0; i < 2 * kStages; ++i)
+      for (uint32_t parity = 0; parity < 2; ++parity)
+        (void)warp_wait(smem_u32(&sh.bars.kv_full[i >> 1][i & 1]), parity, &sh.never);
   }
-  if (!good && (threadIdx.x & 31u) == 0u && sh.abort_flag == 0u) {
+  if (!good && (threadIdx.x & 31u) == 0u && *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) == 0u) {
     *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) = 1u;
     report(p.status, MLA_STATUS_TIMEOUT);
   }
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
 }
 
-// The products of one tile's weights with its values, into the sums.
+// The products of one tile's weights with its values, into the sums: columns 0..255, then 256..511.
 template <bool F16, bool FIRST>
-__device__ __forceinline__ void pv_products(uint64_t p, uint64_t v, uint32_t tmem) {
+__device__ __forceinline__ void pv_half(uint64_t p, uint64_t v, uint32_t tmem, int half) {
   constexpr uint32_t id = instr_desc(F16, 256, true);
+  const uint32_t d = tmem + static_cast<uint32_t>(half) * 128u;
+  const uint64_t vh = v + static_cast<uint64_t>(half * kHalfSlabs * (kSlabBytes >> 4));
+  mma_ws<!FIRST>(d, p, vh, id);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint32_t d = tmem + static_cast<uint32_t>(half) * 128u;
-    const uint64_t vh = v + static_cast<uint64_t>(half * 4 * (kSlabBytes >> 4));
-    mma_ws<!FIRST>(d, p, vh, id);
+  for (int j = 1; j < kKeys / 16; ++j)
+    mma_ws<true>(d, p + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j * 128), id);
+}
+
+template <bool F16, bool FIRST>
+__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st) {
+  pv_half<F16, FIRST>(p, v, tmem, 0);
+  commit(smem_u32(&sh.bars.kv_empty[st][0]));
+  pv_half<F16, FIRST>(p, v, tmem, 1);
+  commit(smem_u32(&sh.bars.kv_empty[st][1]));
+  commit(smem_u32(&sh.bars.pv_done));
+}
+
+// Scores from slab S0 on, N of them (four steps of 16 each); slab 8 counts as the first half's first.
+template <bool F16, int S0, int N, bool FIRST>
+__device__ __forceinline__ void qk_slabs(uint64_t q, uint64_t k, uint32_t d) {
+  constexpr uint32_t id = instr_desc(F16, kKeys, false);
 #pragma unroll
-    for (int j = 1; j < kKeys / 16; ++j)
-      mma_ws<true>(d, p + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j * 128), id);
+  for (int j = 0; j < 4 * N; ++j) {
+    const uint64_t off = static_cast<uint64_t>((S0 + (j >> 2)) * (kSlabBytes >> 4) + (j & 3) * 2);
+    if (FIRST && j == 0) {
+      mma_ws<false>(d, q + off, k + off, id);
+    } else {
+      mma_ws<true>(d, q + off, k + off, id);
+    }
   }
 }
 
@@ -769,13 +859,14 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
   const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
   const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
   uint32_t s = 0, v = 0;        // the next tile to get scores, and sums: v <= s <= v + 2
+  bool begun = false;           // tile s has its first half's scores
   uint32_t seg = 0;             // segments begun
   int left = 0;                 // tiles of the current segment without scores
   bool more = true, first = false;
   uint32_t first_bits = 0;      // bit (i & 1): tile i is its segment's first
   uint32_t v_seg = 0;           // segments whose sums have begun
   uint32_t idle = 0;
-  // whichever has its operands goes: the sums of the oldest tile (they free its
+  // Whichever has its operands goes: the sums of the oldest tile (they free its
   // stage), else the scores of the next.  Waiting for a certain one of the two
   // would let the loaders and the tensor cores wait for each other in turn.
   while (true) {
@@ -793,39 +884,39 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
         fence_after();
         const uint64_t vd = dV + (v & 1u) * (kTileBytes >> 4);
         if (opens) {
-          pv_products<F16, true>(dP, vd, tmem);
+          pv_products<F16, true>(sh, dP, vd, tmem, v & 1u);
           ++v_seg;
         } else {
-          pv_products<F16, false>(dP, vd, tmem);
+          pv_products<F16, false>(sh, dP, vd, tmem, v & 1u);
         }
-        commit(smem_u32(&sh.bars.kv_empty[v & 1u]));
-        commit(smem_u32(&sh.bars.pv_done));
         ++v;
         idle = 0;
         continue;
       }
     }
-    const uint32_t st = s & 1u;
-    if (left > 0 && s < v + 2 && warp_test(smem_u32(&sh.bars.kv_full[st]), (s / kStages) & 1u) &&
+    const uint32_t st = s & 1u, full = (s / kStages) & 1u, d = tmem + kTmemS + 32u * st;
+    const uint64_t k = dK + st * (kTileBytes >> 4);
+    if (left > 0 && !begun && s < v + 2 && warp_test(smem_u32(&sh.bars.kv_full[st][0]), full) &&
         (!first || warp_test(smem_u32(&sh.bars.q_full), (seg - 1) & 1u)) &&
         (s < 2 || warp_test(smem_u32(&sh.bars.s_empty[st]), (s / 2 - 1) & 1u))) {
+      fence_async();  // rows that came by plain asynchronous copies, before the tensor cores read them
       fence_after();
-      constexpr uint32_t id = instr_desc(F16, kKeys, false);
-      const uint64_t k = dK + st * (kTileBytes >> 4);
-#pragma unroll
-      for (int j = 0; j < kD / 16; ++j) {
-        const uint64_t off = static_cast<uint64_t>((j >> 2) * (kSlabBytes >> 4) + (j & 3) * 2);
-        if (j == 0) {
-          mma_ws<false>(tmem + kTmemS + 32u * st, dQ + off, k + off, id);
-        } else {
-          mma_ws<true>(tmem + kTmemS + 32u * st, dQ + off, k + off, id);
-        }
-      }
+      qk_slabs<F16, 8, 1, true>(dQ, k, d);
+      qk_slabs<F16, 0, kHalfSlabs, false>(dQ, k, d);
+      begun = true;
+      idle = 0;
+      continue;
+    }
+    if (begun && warp_test(smem_u32(&sh.bars.kv_full[st][1]), full)) {
+      fence_async();
+      fence_after();
+      qk_slabs<F16, kHalfSlabs, kHalfSlabs, false>(dQ, k, d);
       commit(smem_u32(&sh.bars.s_full[st]));
       --left;
       if (left == 0) commit(smem_u32(&sh.bars.q_empty));
       first_bits = (first_bits & ~(1u << st)) | ((first ? 1u : 0u) << st);
       first = false;
+      begun = false;
       ++s;
       idle = 0;
       continue;
@@ -850,6 +941,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
   const int r = (warp & 1) * 32 + lane;  // this thread's row
   const int half = warp >> 1;            // its half of the keys (scores) and of each 256 columns (sums)
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+  const bool negative = scale2 < 0.0f;  // then the scores change sign, and the scale
+  scale2 = fabsf(scale2);
   volatile uint32_t* ab = &sh.abort_flag;
   Segment seg;
   uint32_t it = 0;
@@ -860,11 +953,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
       const uint32_t st = it & 1u;
       good = warp_wait(smem_u32(&sh.bars.s_full[st]), (it / 2) & 1u, ab) && good;
-      // all four warps leave together: a wait that ran out in one is seen by all here
-      if (bar_or(1, 32 * kSoftWarps, !good)) {
-        good = false;
-        break;
-      }
+      // complete by now; the flags may have come through it by the copy engine
+      good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), (it / kStages) & 1u, ab) && good;
       fence_after();
       uint32_t v[32];
       tmem_ld32(tmem + kTmemS + 32u * st + lanes, v);
@@ -872,22 +962,33 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[st]));
-      float s[32];
-      float top = -INFINITY;
+      if (negative) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]) * scale2;
-      if ((va.x & va.y & va.z & va.w & vb.x & vb.y & vb.z & vb.w) != 0x01010101u) {
-        const uint32_t ok[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? s[j] : -INFINITY;
+        for (int j = 0; j < 32; ++j) v[j] ^= 0x80000000u;
       }
+      const bool whole = (va.x & va.y & va.z & va.w & vb.x & vb.y & vb.z & vb.w) == 0x01010101u;
+      const uint32_t ok[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+      if (!whole) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) top = fmaxf(top, s[j]);
+        for (int j = 0; j < 32; ++j) v[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? v[j] : 0xff800000u;
+      }
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        t[j] = fmaxf(fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 8])),
+                     fmaxf(__uint_as_float(v[j + 16]), __uint_as_float(v[j + 24])));
+      const float raw = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+      const float top = raw == -INFINITY ? -INFINITY : raw * scale2;  // scale2 >= 0: the largest score
       const bool first = kt == seg.k0;
-      // products into the sums run until pv_done of the previous tile
-      const bool moved = bar_or(1, 32 * kSoftWarps, first || top > m + kRescale);
+      // One vote a tile: whether a row's reference must move, or a wait ran out
+      // (then all four warps leave together).
+      const bool moved = bar_or(1, 32 * kSoftWarps, first || top > m + kRescale || !good);
       float factor = 1.0f;
       if (moved) {
+        if (bar_or(2, 32 * kSoftWarps, !good)) {
+          good = false;
+          break;
+        }
         sh.xch[half][r] = top;
         bar_sync(2, 32 * kSoftWarps);
         const float next = fmaxf(m, fmaxf(top, sh.xch[half ^ 1][r]));
@@ -897,16 +998,23 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       }
       const float ref = m == -INFINITY ? 0.0f : m;
       uint32_t w[16];
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float a = exp2_fast(s[2 * j] - ref), b = exp2_fast(s[2 * j + 1] - ref);
-        l += a + b;
+        float a = exp2_fast(fmaf(__uint_as_float(v[2 * j]), scale2, -ref));
+        float b = exp2_fast(fmaf(__uint_as_float(v[2 * j + 1]), scale2, -ref));
+        if (!whole) {  // (a zero scale makes no weight of a masked score)
+          a = (ok[j >> 1] >> (16 * (j & 1))) & 1u ? a : 0.0f;
+          b = (ok[j >> 1] >> (16 * (j & 1) + 8)) & 1u ? b : 0.0f;
+        }
+        sum[j & 3] += a + b;
         if constexpr (F16) {
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(b), "f"(a));
         } else {
           w[j] = pack_bf16x2(a, b);
         }
       }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (it > 0) {  // the previous tile's weights have been read, its products are in the sums
         good = warp_wait(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
       }
@@ -1000,7 +1108,9 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
     if (w < warp) before += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  const int64_t each = total > p.ctas ? (total + p.ctas - 1) / p.ctas : 1;
+  // at least a tile's cost, so that every CTA between a row tile's first and last has one of its key tiles
+  const int64_t least = p.tile_cost > kCostImage ? p.tile_cost : kCostImage;
+  const int64_t each = (total + p.ctas - 1) / p.ctas > least ? (total + p.ctas - 1) / p.ctas : least;
   Cursor c;
   c.pos = each * blockIdx.x;
   c.end = c.pos + each < total ? c.pos + each : total;
@@ -1027,7 +1137,8 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
 
 template <int FMT, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
-  constexpr uint32_t kFillWarps = FMT == MLA_CACHE_BF16 ? kLoadWarps : kLoadWarps / 2;  // that fill one tile
+  // a half of a tile: one arrival a warp, or one a thread and one a warp
+  constexpr uint32_t kFill = FMT == MLA_CACHE_BF16 ? 33 * kLoadWarps : kLoadWarps;
   extern __shared__ uint8_t dsmem[];
   __shared__ Shared sh;
   const int warp = uniform(static_cast<int>(threadIdx.x) >> 5);
@@ -1049,12 +1160,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
     };
     for (int i = 0; i < 2; ++i) {
-      init(&sh.bars.kv_full[i], kFillWarps);
-      init(&sh.bars.kv_empty[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        init(&sh.bars.kv_full[i][h], kFill);
+        init(&sh.bars.kv_empty[i][h], 1);
+      }
       init(&sh.bars.s_full[i], 1);
       init(&sh.bars.s_empty[i], kSoftWarps);
     }
-    init(&sh.bars.q_full, kFillWarps);
+    init(&sh.bars.q_full, 32 * kLoadWarps);
     init(&sh.bars.q_empty, 1);
     init(&sh.bars.p_full, kSoftWarps);
     init(&sh.bars.pv_done, 1);
@@ -1089,21 +1202,80 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
   }
 }
 
+// ---- decoded prefix tiles -------------------------------------------------------------
+//
+// A prefix of a group with many rows is read by many CTAs, 64 rows at a time.
+// It is decoded once, into tiles as they lie in shared memory (swizzled 16-bit
+// values, zeros where there is no key, and a flag for each key); the attention
+// kernel then fetches a tile half with two or three bulk copies.  One block a
+// tile; blocks behind a prefix's end leave.
+template <int FMT, bool F16>
+__global__ void __launch_bounds__(256) image_kernel(const Params p) {
+  pdl_wait();
+  const int64_t g = blockIdx.y;
+  bool bad;
+  const Unit x = unit_at(p, g, bad);
+  const int64_t kt = blockIdx.x;
+  if (kt < x.key_tiles() && x.rows > 0) {
+    const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+    const int row0 = 8 * warp;
+    uint8_t* dst = p.image + (g * p.image_tiles + kt) * kImageBytes;
+    KeyAt at;
+    bool bad_page = false;
+    at.fetch(p, x.table, static_cast<int32_t>(x.len), static_cast<int32_t>(kt), row0 + lane, lane < 8);
+    const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
+    auto put = [&](int s, int r, int c, const uint4& v) {
+      *reinterpret_cast<uint4*>(dst + piece_addr(0, s, r, c)) = v;
+    };
+    if constexpr (FMT == MLA_CACHE_BF16) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 v[18];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4* src = reinterpret_cast<const uint4*>(row_at(mine, i));
+        v[2 * i] = src != nullptr ? __ldcg(src + lane) : zero;
+        v[2 * i + 1] = src != nullptr ? __ldcg(src + 32 + lane) : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4* src = reinterpret_cast<const uint4*>(row_at(mine, 4 * i + (lane >> 3)));
+        v[16 + i] = src != nullptr ? __ldcg(src + 64 + (lane & 7)) : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        put(lane >> 3, row0 + i, lane & 7, v[2 * i]);
+        put(4 + (lane >> 3), row0 + i, lane & 7, v[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) put(8, row0 + 4 * i + (lane >> 3), lane & 7, v[16 + i]);
+    } else {
+      Raw<FMT> raw;
+      load_rows<FMT>(raw, mine, lane);
+      store_half<FMT, F16>(raw, 0, row0, lane, put);
+      store_half<FMT, F16>(raw, 1, row0, lane, put);
+    }
+    if (lane < 8) dst[kTileBytes + row0 + lane] = mine != nullptr ? 1 : 0;
+    if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
+  }
+  pdl_trigger();
+}
+
 // ---- joining a row's segments ----------------------------------------------------------
 //
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A block takes one token,
-// 16 of its heads and a slice of the columns; thread (row, worker).  The
-// workers of a row first share out its segments for the weights, then its
-// (column chunk, segment class) pairs for the sum.  With few tokens the
-// columns are cut into more slices and the segments into classes, so that a
-// single row's many segments are still read by many threads.
+// 16 of its heads and a slice of the columns; thread (row, worker).  A thread's
+// first sums are loaded before the weights they need are known, so the chain is
+// plan, statistics and sums: few trips to memory, whatever n is.  With few
+// tokens the columns are cut into more slices and a row's segments shared out
+// to classes of workers.
 
 constexpr int kJoinRows = 16, kJoinWorkers = 16, kJoinThreads = kJoinRows * kJoinWorkers;
+constexpr int kJoinAhead = 6;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int slices) {
   extern __shared__ float weights[];  // [segments][16]
-  __shared__ float red[kJoinWorkers][kJoinRows];
-  __shared__ uint4 sums[kJoinWorkers][kJoinRows];
+  __shared__ float red[2][kJoinWorkers][kJoinRows];
+  __shared__ float4 sums[kJoinWorkers][kJoinRows];
   pdl_wait();
   const int row = static_cast<int>(threadIdx.x) % kJoinRows, wk = static_cast<int>(threadIdx.x) / kJoinRows;
   const int head_blocks = (p.H + kJoinRows - 1) / kJoinRows;
@@ -1116,8 +1288,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
 
   // the row's segments: n1 of its group's prefix, n2 of its own keys
   const int64_t each = __ldcg(p.plan);
-  int64_t n1 = 0, n2 = 0, at1 = 0, at2 = 0;
-  int prow = 0;
+  int64_t at1 = 0, at2 = 0;
+  int n1 = 0, n2 = 0, prow = 0;
   const int orow = h % kRowsTile;
   if (live) {
     int64_t g = -1;
@@ -1131,109 +1303,127 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
       }
       g = lo - 1;
     }
+    // CTAs c0 .. c1 have the row's key tiles
+    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int64_t& at, int& n) {
+      const int64_t per = x.row_cost();
+      if (per == 0) return;
+      const int64_t f = __ldcg(p.plan + 1 + unit) + tile * per;
+      const int64_t c0 = (f + kCostSegment) / each, c1 = (f + per - x.tile_cost) / each;
+      at = c0 + x.part0 + tile;
+      n = static_cast<int>(c1 - c0) + 1;
+    };
     bool bad;
+    const Unit own = unit_at(p, p.G + t, bad);
+    span(own, p.G + t, h / kRowsTile, at2, n2);
     if (g >= 0) {
       const Unit x = unit_at(p, g, bad);
-      const int64_t i = t * p.H + h - x.rows0, per = x.row_cost();
-      if (i >= 0 && i < x.rows && per > 0) {
-        const int64_t tile = i / kRowsTile, f = __ldcg(p.plan + 1 + g) + tile * per;
-        const int64_t c0 = (f + kSegCost) / each;  // the CTA that has the first key tile
-        at1 = c0 + x.part0 + tile;
-        n1 = (f + per - 1) / each - c0 + 1;
+      const int64_t i = t * p.H + h - x.rows0;
+      if (i >= 0 && i < x.rows) {
+        span(x, g, i / kRowsTile, at1, n1);
         prow = static_cast<int>(i % kRowsTile);
       }
     }
-    const Unit x = unit_at(p, p.G + t, bad);
-    const int64_t per = x.row_cost(), tile = h / kRowsTile;
-    if (per > 0) {
-      const int64_t f = __ldcg(p.plan + 1 + p.G + t) + tile * per;
-      const int64_t c0 = (f + kSegCost) / each;
-      at2 = c0 + x.part0 + tile;
-      n2 = (f + per - 1) / each - c0 + 1;
-    }
   }
-  const int n = static_cast<int>(n1 + n2);
-  auto part_of = [&](int i, int& rows, int& r) -> const uint8_t* {
-    if (i < n1) {
-      rows = kRowsTile;
-      r = prow;
-      return p.prefix_part + (at1 + i) * part_bytes(kRowsTile);
-    }
-    rows = p.own_rows;
-    r = orow;
-    return p.own_part + (at2 + i - n1) * part_bytes(p.own_rows);
+  const int n = n1 + n2;
+  // segment i: its sums, and its statistics
+  auto sums_of = [&](int i, int chunk) -> float4 {
+    const bool pre = i < n1;
+    const uint8_t* part = pre ? p.prefix_part + (at1 + i) * part_bytes(kRowsTile)
+                              : p.own_part + (at2 + i - n1) * part_bytes(p.own_rows);
+    return __ldcg(reinterpret_cast<const float4*>(part) + static_cast<int64_t>(chunk) * (pre ? kRowsTile : p.own_rows) +
+                  (pre ? prow : orow));
+  };
+  auto stats_of = [&](int i, float& m, float& l) {
+    const bool pre = i < n1;
+    const int rows = pre ? kRowsTile : p.own_rows;
+    const uint8_t* part = pre ? p.prefix_part + (at1 + i) * part_bytes(kRowsTile)
+                              : p.own_part + (at2 + i - n1) * part_bytes(p.own_rows);
+    const float* s = reinterpret_cast<const float*>(part + static_cast<int64_t>(rows) * kChunks * 16) + (pre ? prow : orow);
+    m = __ldcg(s);
+    l = __ldcg(s + rows);
   };
 
+  // `per` chunks of 4 columns in this slice, cw of them at a time, 16 / cw segment classes
+  const int per = kChunks / slices;
+  const int cw = per < kJoinWorkers ? per : kJoinWorkers;
+  const int classes = kJoinWorkers / cw;
+  const int cls = wk / cw;
+  const int chunk0 = slice * per + wk % cw;
+  float4 ahead[kJoinAhead];
+#pragma unroll
+  for (int j = 0; j < kJoinAhead; ++j) {
+    const int i = cls + j * classes;
+    ahead[j] = i < n ? sums_of(i, chunk0) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+
   // ---- weights
-  float top = -INFINITY;
-  for (int i = wk; i < n; i += kJoinWorkers) {
-    int rows, r;
-    const uint8_t* part = part_of(i, rows, r);
-    const float m = __ldcg(reinterpret_cast<const float*>(part + static_cast<int64_t>(rows) * kChunks * 16) + r);
-    weights[i * kJoinRows + row] = m;
+  float top = -INFINITY, m0 = -INFINITY, l0 = 0.0f;
+  if (wk < n) stats_of(wk, m0, l0);
+  top = m0;
+  for (int i = wk + kJoinWorkers; i < n; i += kJoinWorkers) {
+    float m, l;
+    stats_of(i, m, l);
     top = fmaxf(top, m);
   }
-  red[wk][row] = top;
+  red[0][wk][row] = top;
   __syncthreads();
-  for (int i = 0; i < kJoinWorkers; ++i) top = fmaxf(top, red[i][row]);
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinWorkers; ++i) top = fmaxf(top, red[0][i][row]);
   const float ref = top == -INFINITY ? 0.0f : top;
   float den = 0.0f;
   for (int i = wk; i < n; i += kJoinWorkers) {
-    int rows, r;
-    const uint8_t* part = part_of(i, rows, r);
-    const float l = __ldcg(reinterpret_cast<const float*>(part + static_cast<int64_t>(rows) * kChunks * 16) + rows + r);
-    const float w = exp2f(weights[i * kJoinRows + row] - ref);
+    float m = m0, l = l0;
+    if (i != wk) stats_of(i, m, l);
+    const float w = exp2f(m - ref);
     weights[i * kJoinRows + row] = w;
     den += w * l;
   }
-  red[wk][row] = den;
+  red[1][wk][row] = den;
   __syncthreads();
   den = 0.0f;
-  for (int i = 0; i < kJoinWorkers; ++i) den += red[i][row];
+#pragma unroll
+  for (int i = 0; i < kJoinWorkers; ++i) den += red[1][i][row];
   if (live && slice == 0 && wk == 0 && p.lse != nullptr)
     p.lse[t * p.H + h] = den > 0.0f || den != den ? (ref + log2f(den)) * 0.6931471805599453f : -INFINITY;
   float mul = den > 0.0f || den != den ? 1.0f / den : 0.0f;
   if (p.kv_scale != nullptr) mul *= __ldcg(p.kv_scale);
 
-  // ---- sums: `per` chunks of 4 columns in this slice, cw of them at a time, 16 / cw segment classes
-  const int per = kChunks / slices;
-  const int cw = per < kJoinWorkers ? per : kJoinWorkers;
-  const int classes = kJoinWorkers / cw;
-  const int cls = wk / cw;
+  // ---- sums
   for (int c0 = 0; c0 < per; c0 += cw) {
-    const int chunk = slice * per + c0 + wk % cw;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = cls; i < n; i += classes) {
-      int rows, r;
-      const uint8_t* part = part_of(i, rows, r);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + static_cast<int64_t>(chunk) * rows + r);
+    auto add = [&](int i, const float4& o) {
       const float w = weights[i * kJoinRows + row];
       acc.x += w * o.x;
       acc.y += w * o.y;
       acc.z += w * o.z;
       acc.w += w * o.w;
+    };
+    int i = cls;
+    if (c0 == 0) {
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j, i += classes)
+        if (i < n) add(i, ahead[j]);
     }
+#pragma unroll 4
+    for (; i < n; i += classes) add(i, sums_of(i, chunk0 + c0));
     if (classes > 1) {
       __syncthreads();
-      sums[wk][row] = make_uint4(__float_as_uint(acc.x), __float_as_uint(acc.y), __float_as_uint(acc.z),
-                                 __float_as_uint(acc.w));
+      sums[wk][row] = acc;
       __syncthreads();
       if (cls == 0) {
-        for (int i = 1; i < classes; ++i) {
-          const uint4 o = sums[i * cw + wk % cw][row];
-          acc.x += __uint_as_float(o.x);
-          acc.y += __uint_as_float(o.y);
-          acc.z += __uint_as_float(o.z);
-          acc.w += __uint_as_float(o.w);
+        for (int k = 1; k < classes; ++k) {
+          const float4 o = sums[k * cw + wk % cw][row];
+          acc.x += o.x;
+          acc.y += o.y;
+          acc.z += o.z;
+          acc.w += o.w;
         }
       }
     }
     if (live && cls == 0) {
       uint2 o = make_uint2(pack_bf16x2(acc.x * mul, acc.y * mul), pack_bf16x2(acc.z * mul, acc.w * mul));
       if (n == 0) o = make_uint2(0, 0);
-      *reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kDv + 4 * chunk) = o;
+      *reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kDv + 4 * (chunk0 + c0)) = o;
     }
   }
   pdl_trigger();
@@ -1241,24 +1431,38 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
 
 // ---- host ------------------------------------------------------------------------------
 
+// A prefix is decoded once, into the workspace, when its group has at least
+// kImageRows rows on average and the images fit kImageLimit; else its tiles
+// are read from the cache.
+constexpr int64_t kImageRows = 4 * kRowsTile;
+constexpr int64_t kImageLimit = INT64_C(1) << 31;
+
 struct Layout {
-  int64_t prefix_part, own_part, bytes;
+  int64_t prefix_part, own_part, image, image_tiles, bytes;
 };
 
-Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t ctas) {
+Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t ctas) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout l;
   l.prefix_part = up(8 * (1 + G + T));
   const int64_t prefix_parts = G > 0 ? T * H / kRowsTile + G + 1 + ctas : 0;
   l.own_part = up(l.prefix_part + prefix_parts * part_bytes(kRowsTile));
   const int64_t own_parts = T * ((H + kRowsTile - 1) / kRowsTile) + ctas;
-  l.bytes = up(l.own_part + own_parts * part_bytes(static_cast<int>(H < kRowsTile ? H : kRowsTile)));
+  l.image = up(l.own_part + own_parts * part_bytes(static_cast<int>(H < kRowsTile ? H : kRowsTile)));
+  l.image_tiles = (prefix_keys + kKeys - 1) / kKeys;
+  if (G < 1 || G > 65535 || T * H < kImageRows * G || l.image_tiles > kImageLimit / kImageBytes / G) l.image_tiles = 0;
+  l.bytes = up(l.image + G * l.image_tiles * kImageBytes);
   return l;
 }
 
 template <int FMT, bool F16>
 const void* kernel_for() {
   return reinterpret_cast<const void*>(&attend_kernel<FMT, F16>);
+}
+
+template <int FMT, bool F16>
+const void* image_for() {
+  return reinterpret_cast<const void*>(&image_kernel<FMT, F16>);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -1269,10 +1473,9 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G) {
   return T >= 0 && H >= 1 && H <= 65535 && T <= (static_cast<int64_t>(INT_MAX) - kRowsTile) / H && G >= 0 && G <= T;
 }
 
-mla_status launch(const void* fn, int64_t blocks, int threads, size_t smem, bool pdl, mla_stream_t stream,
-                  void** args) {
+mla_status launch(const void* fn, dim3 grid, int threads, size_t smem, bool pdl, mla_stream_t stream, void** args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -1292,14 +1495,16 @@ mla_status launch(const void* fn, int64_t blocks, int threads, size_t smem, bool
 
 extern "C" {
 
-mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int32_t sm_count, int64_t* bytes) {
+mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t sm_count,
+                                       int64_t* bytes) {
   using namespace mla::attend;
-  if (bytes == nullptr || !sizes_ok(T, H, G)) return MLA_ERR_INVALID_ARG;
+  if (bytes == nullptr || !sizes_ok(T, H, G) || prefix_keys < 0 || prefix_keys > (INT64_C(1) << 62))
+    return MLA_ERR_INVALID_ARG;
   if (sm_count <= 0) {
     const mla_status s = mla::current_device(nullptr, &sm_count);
     if (s != MLA_OK) return s;
   }
-  *bytes = layout_of(T, H, G, sm_count).bytes;
+  *bytes = layout_of(T, H, G, prefix_keys, sm_count).bytes;
   return MLA_OK;
 }
 
@@ -1340,7 +1545,7 @@ mla_status mla_prefix_attend_launch(
   int32_t sms = 0;
   mla_status s = mla::current_device(&dev, &sms);
   if (s != MLA_OK) return s;
-  const Layout lay = layout_of(T, H, G, sms);
+  const Layout lay = layout_of(T, H, G, prefix_cols * block_size, sms);
   if (workspace_bytes < lay.bytes) return MLA_ERR_INVALID_ARG;
 
   Params p;
@@ -1371,10 +1576,13 @@ mla_status mla_prefix_attend_launch(
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.plan = reinterpret_cast<int64_t*>(ws);
+  p.image = lay.image_tiles > 0 ? ws + lay.image : nullptr;
+  p.image_tiles = lay.image_tiles;
   p.prefix_part = ws + lay.prefix_part;
   p.own_part = ws + lay.own_part;
   p.own_rows = static_cast<int32_t>(H < kRowsTile ? H : kRowsTile);
   p.ctas = sms;
+  p.tile_cost = format == MLA_CACHE_BF16 ? kCostRows : kCostCodes;
   p.status = status;
 
   static const void* const kernels[4] = {kernel_for<MLA_CACHE_BF16, false>(), kernel_for<MLA_CACHE_E4M3, false>(),
@@ -1388,15 +1596,25 @@ mla_status mla_prefix_attend_launch(
     g_smem_ready[dev][k].store(true, std::memory_order_release);
   }
   void* args[] = {&p};
-  s = launch(kernels[k], sms, kThreads, kSmemBytes, (flags & MLA_FLAG_PDL) != 0, stream, args);
+  bool pdl = (flags & MLA_FLAG_PDL) != 0;
+  if (p.image != nullptr) {
+    static const void* const images[4] = {image_for<MLA_CACHE_BF16, false>(), image_for<MLA_CACHE_E4M3, false>(),
+                                          image_for<MLA_CACHE_MX, false>(), image_for<MLA_CACHE_E4M3, true>()};
+    s = launch(images[k], dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
+               args);
+    if (s != MLA_OK) return s;
+    pdl = true;
+  }
+  s = launch(kernels[k], dim3(static_cast<unsigned>(sms), 1, 1), kThreads, kSmemBytes, pdl, stream, args);
   if (s != MLA_OK) return s;
 
+  // slices: enough blocks for every SM to have some, a thread not below one chunk of columns
   const int64_t rows = T * ((H + kJoinRows - 1) / kJoinRows);
   int32_t slices = 1;
-  while (slices < 32 && rows * slices < 8 * sms) slices *= 2;
+  while (slices < 32 && rows * slices < 2 * sms) slices *= 2;
   void* jargs[] = {&p, &slices};
-  return launch(reinterpret_cast<const void*>(&join_kernel), rows * slices, kJoinThreads,
-                static_cast<size_t>(2 * sms) * kJoinRows * sizeof(float), true, stream, jargs);
+  return launch(reinterpret_cast<const void*>(&join_kernel), dim3(static_cast<unsigned>(rows * slices), 1, 1),
+                kJoinThreads, static_cast<size_t>(2 * sms) * kJoinRows * sizeof(float), true, stream, jargs);
 }
 
 }  // extern "C"

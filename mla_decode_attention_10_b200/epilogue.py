@@ -115,7 +115,7 @@ def lib() -> ctypes.CDLL:
         L.mla_latent_gather_launch.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64, i64, u32, vp, i64,
                                                vp, vp]
         L.mla_prefix_attend_workspace.restype = ctypes.c_int
-        L.mla_prefix_attend_workspace.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
+        L.mla_prefix_attend_workspace.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(i64)]
         L.mla_prefix_attend_launch.restype = ctypes.c_int
         L.mla_prefix_attend_launch.argtypes = [vp, i64, i64, vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64,
                                                vp, i64, i64, vp, i64, i64, ctypes.c_float, u32, vp, vp, vp, i64,
@@ -223,10 +223,11 @@ def mla_latent_gather_launch(cache, format, block_size, num_blocks, kv_scale, bl
                                           table_cols, cu_rows, first, B, N, flags, out, out_stride, status, stream)
 
 
-def mla_prefix_attend_workspace(T: int, H: int, G: int, sm_count: int = 0) -> int:
-    """Bytes of workspace mla_prefix_attend_launch needs (sm_count 0: of the current device)."""
+def mla_prefix_attend_workspace(T: int, H: int, G: int, prefix_keys: int = 0, sm_count: int = 0) -> int:
+    """Bytes of workspace mla_prefix_attend_launch needs (prefix_keys: pages of a prefix table row times the block
+    size; sm_count 0: of the current device)."""
     n = ctypes.c_int64()
-    rc = lib().mla_prefix_attend_workspace(T, H, G, sm_count, ctypes.byref(n))
+    rc = lib().mla_prefix_attend_workspace(T, H, G, prefix_keys, sm_count, ctypes.byref(n))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_prefix_attend_workspace")
     return n.value

@@ -19,6 +19,7 @@ allocator on that stream.  Wrong arguments raise ``ValueError`` here or
 
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -191,6 +192,9 @@ def _sm_count(index: int) -> int:
     return n
 
 
+_workspace_bytes = functools.lru_cache(maxsize=256)(E.mla_prefix_attend_workspace)
+
+
 def mla_prefix_decode_attention(
         q: torch.Tensor, cache: torch.Tensor, block_table: Optional[torch.Tensor],
         seq_lens: Optional[torch.Tensor], *, sm_scale: float,
@@ -247,7 +251,7 @@ def mla_prefix_decode_attention(
     if lse is None:
         lse = _empty((T, H), _F32, index, stream)
     if workspace is None:
-        workspace = _empty((E.mla_prefix_attend_workspace(T, H, G, _sm_count(index)),), _U8, index, stream)
+        workspace = _empty((_workspace_bytes(T, H, G, pcols * cache.shape[1], _sm_count(index)),), _U8, index, stream)
     elif workspace.dim() != 1:
         raise ValueError("workspace must be a one-dimensional uint8 tensor")
     _launch(index, "mla_prefix_attend_launch", E.lib().mla_prefix_attend_launch,

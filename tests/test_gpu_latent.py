@@ -316,7 +316,8 @@ class _Case:
 
 def _run(case, **kw):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    need = E.mla_prefix_attend_workspace(len(case.lens), case.H, len(case.prefixes))
+    cap = case.prefix_table.shape[1] * case.block if case.prefixes else 0
+    need = E.mla_prefix_attend_workspace(len(case.lens), case.H, len(case.prefixes), cap)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN throughout
     out, lse = case.call(status=status, workspace=ws, **kw)
     torch.cuda.synchronize()
