@@ -54,26 +54,56 @@ namespace attend {
 
 constexpr int kRowsTile = 64;   // rows of a CTA (MMA M)
 constexpr int kKeys = 64;       // keys of a tile
-constexpr int kD = 576;         // score contraction
 constexpr int kDv = 512;        // values
-constexpr int kSlabs = 9;       // 64-wide column slabs of a 576-wide row
-constexpr uint32_t kSlabBytes = 64 * 128;               // 64 rows x 64 values of 16 bits
-constexpr uint32_t kTileBytes = kSlabs * kSlabBytes;    // 72 KB
-constexpr uint32_t kPBytes = kRowsTile * kKeys * 2;     // 8 KB
-constexpr int kStages = 2;
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kLoadWarp0 = 5, kLoadWarps = 8;
-constexpr int kThreads = 32 * (kLoadWarp0 + kLoadWarps);  // 416
-constexpr uint32_t kSmemBytes = kTileBytes * (1 + kStages) + kPBytes + 1024;
+constexpr uint32_t kSlabBytes = 64 * 128;  // one 128-byte column slab of 64 rows, 128-byte swizzle
+
+// Operand forms.  kBf16: q and keys as bf16, weights as bf16.  kF8: q and keys as
+// the e4m3 codes they are stored in, weights as three e5m2 terms (hi + mid + lo:
+// each takes three of the weight's bits, nine in all against bf16's eight).
+enum Op { kBf16 = 0, kF8 = 1 };
+
+// A tile in shared memory: 128-byte slabs of its rows, the 512 values first, then
+// the rotary slab (in kF8 half full).  It is filled, used and freed in two
+// halves: the first half of the values with the rotary slab, and the rest.
+template <int OP>
+struct Shape {
+  static constexpr int kElem = OP == kF8 ? 1 : 2;
+  static constexpr int kHalfSlabs = OP == kF8 ? 2 : 4;
+  static constexpr int kPeSlab = 2 * kHalfSlabs;
+  static constexpr int kPeSteps = OP == kF8 ? 2 : 4;        // MMAs over the rotary slab, 32 bytes of a row each
+  static constexpr int kTerms = OP == kF8 ? 3 : 1;          // weights
+  static constexpr int kKeySteps = OP == kF8 ? 2 : 4;       // MMAs over a tile's keys, 32 or 16 keys each
+  static constexpr uint32_t kTile = (kPeSlab + 1) * kSlabBytes;          // 72 or 40 KB
+  static constexpr uint32_t kP = OP == kF8 ? 2 * kSlabBytes : kSlabBytes;
+  static constexpr int kStages = OP == kF8 ? 4 : 2;
+  static constexpr uint32_t kSmem = kTile * (1 + kStages) + kP + 1024;
+  static constexpr uint32_t kImage = kTile + 128;           // a decoded tile as it lies in shared memory, then its 64 flags
+};
+constexpr int kMaxStages = 4;
+
+// Roles.  Rows that need no decoding come by asynchronous copies, which four
+// warps issue easily, and leave eight warps for the softmax; decoding rows
+// takes eight warps.
+template <int FMT, int OP>
+struct Roles {
+  static constexpr bool kDecode = OP == kBf16 && FMT != MLA_CACHE_BF16;
+  static constexpr int kSoft = kDecode ? 4 : 8;
+  static constexpr int kMma = kSoft;
+  static constexpr int kLoad0 = kSoft + 1;
+  static constexpr int kLoad = kDecode ? 8 : 4;
+  static constexpr int kRows = kRowsTile / kLoad;           // rows of a loader warp
+};
+constexpr int kThreads = 32 * 13;
+
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kWaitSpins = 1u << 22;
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
+constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
-constexpr int kHalfSlabs = 4;          // slabs of a tile's second half; the first half has the rotary slab too
-constexpr uint32_t kImageBytes = kTileBytes + 128;  // a decoded tile as it lies in shared memory, then its 64 flags
-// What the deal counts (measured cycles, in hundreds): a key tile of a decoded
-// prefix, one read from the cache, and a segment's start and end.
-constexpr int kCostImage = 30, kCostRows = 36, kCostCodes = 44, kCostSegment = 70;
+// What the deal counts (measured cycles, in hundreds): a key tile, by how it
+// comes, and a segment's start and end.
+constexpr int kCostImage = 30, kCostRows = 36, kCostCodes = 60, kCostF8 = 22, kCostSegment = 70;
 
 struct Params {
   const uint8_t* q;
@@ -102,7 +132,8 @@ struct Params {
   uint8_t* own_part;
   int32_t own_rows;   // rows of an own segment: min(H, 64)
   int32_t ctas;       // CTAs of the attention kernel
-  int32_t tile_cost;  // of a tile read from the cache
+  int32_t image_bytes;  // of one tile's image
+  int32_t tile_cost, image_cost;  // of a tile read from the cache, from an image
   int32_t* status;
 };
 
@@ -175,7 +206,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
     x.rows0 = lo * p.H;
     x.rows = (hi - lo) * p.H;
     x.table = p.prefix_table + u * p.prefix_stride;
-    x.image = p.image != nullptr ? p.image + u * p.image_tiles * kImageBytes : nullptr;
+    x.image = p.image != nullptr ? p.image + u * p.image_tiles * p.image_bytes : nullptr;
     x.prefix = true;
     x.part0 = x.rows0 / kRowsTile + u;
   } else {
@@ -192,7 +223,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
   }
   bad = bad || len > keys;
   x.len = cut(len, 0, keys);
-  x.tile_cost = x.image != nullptr ? kCostImage : p.tile_cost;
+  x.tile_cost = x.image != nullptr ? p.image_cost : p.tile_cost;
   return x;
 }
 
@@ -256,11 +287,14 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (static_cast<uint64_t>(sbo >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
-// Instruction descriptor of kind::f16, fp32 accumulator: operands fp16 (0) or
-// bf16 (1), M = 64; b_mn: B is MN-major.
-__device__ __forceinline__ constexpr uint32_t instr_desc(bool f16, int n, bool b_mn) {
-  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRowsTile >> 4) << 24);
+// Instruction descriptor, fp32 accumulator, M = 64.  kBf16: both operands bf16
+// (kind::f16).  kF8 (kind::f8f6f4): B e4m3, A e4m3 (q) or e5m2 (weights).
+// b_mn: B is MN-major.
+template <int OP>
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn) {
+  const uint32_t at = OP == kBf16 ? 1u : (b_mn ? 1u : 0u), bt = OP == kBf16 ? 1u : 0u;
+  return (1u << 4) | (at << 7) | (bt << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(kRowsTile >> 4) << 24);
 }
 
 // One MMA, issued by one lane of the warp.  The warp stays converged, and
@@ -269,15 +303,25 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(bool f16, int n, bool b
 // registers.  Issued from a branch on the lane, each MMA first moved its
 // descriptors there: 50 to 65 cycles, where the N = 64 form takes 32 (the 4 KB
 // of its operands at 128 bytes a cycle).
-template <bool ACCUMULATE>
+template <int OP, bool ACCUMULATE>
 __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
-      : "memory");
+  if constexpr (OP == kBf16) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        : "memory");
+  }
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -308,9 +352,13 @@ __device__ __forceinline__ void arrive(uint32_t bar, uint32_t count = 1) {
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 32 columns of this warp's TMEM lanes, one lane's per thread; the wait names
+// 32 or 16 columns of this warp's TMEM lanes, one lane's per thread; the wait names
 // the registers, so no use of them can be scheduled before it.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]);
+
+template <>
+__device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -330,6 +378,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
                : "memory");
 }
 
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15])
+               :
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -341,10 +406,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Whether the phase of `parity` has completed.  One lane asks (32 lanes' asking
-// costs 32 times as much of the shared-memory pipe, which the operands and the
-// loaders need), the warp stays converged and gets one answer.
-__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+// Whether the phase of `parity` has completed, as bit `bit`, in the lane that
+// asks.  One lane asks (32 lanes' asking costs 32 times as much of the
+// shared-memory pipe); the MMA warp asks for all it might need at once and
+// joins the answers with one reduction, so that a round costs one trip.
+__device__ __forceinline__ uint32_t ask(uint32_t bar, uint32_t parity, int bit) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -355,7 +421,7 @@ __device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  return __any_sync(0xffffffffu, done != 0u) != 0;
+  return done << bit;
 }
 
 // Waits for the phase, at most kWaitSpins tries or until another role gave up.
@@ -399,6 +465,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Two fp16 -> two e5m2 (ties to even), in the low half; and back.
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t c) { return __byte_perm(c, 0u, 0x1404); }
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 __device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -431,10 +511,8 @@ __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// A tile is filled, used and freed in two halves: slabs 0..3 with the rotary
-// slab 8, and slabs 4..7.
 struct Bars {
-  uint64_t kv_full[kStages][2], kv_empty[kStages][2];
+  uint64_t kv_full[kMaxStages][2], kv_empty[kMaxStages][2];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, o_empty;
@@ -452,22 +530,50 @@ struct Shared {
   uint32_t tmem;
   uint32_t abort_flag;
   uint32_t never;  // stays 0
-  alignas(16) uint8_t valid[kStages][kKeys];  // 1: the key counts, by stage
-  float xch[2][kRowsTile];
+  alignas(16) uint8_t valid[kMaxStages][kKeys];  // 1: the key counts, by stage
+  float xch[4][kRowsTile];
   int64_t warp_sum[kThreads / 32];
   int64_t first_unit, first_base;
 };
 
 // ---- the loaders' pieces --------------------------------------------------------
 //
-// A warp has eight rows of a tile.  Its lanes read along the rows (256 or 512
-// contiguous bytes at a time): with a few lanes on each of eight rows the same
-// loads took four times as many passes through the load pipe.
+// A warp has eight or sixteen rows of a tile.  Its lanes read along the rows (256
+// or 512 contiguous bytes at a time): with a few lanes on each of eight rows the
+// same loads took four times as many passes through the load pipe.
 
 // Piece `c` (0..7) of slab `s` of row r in a tile at `base`.
 __device__ __forceinline__ uint32_t piece_addr(uint32_t base, int s, int r, int c) {
   return base + static_cast<uint32_t>(s) * kSlabBytes + static_cast<uint32_t>(r) * 128u +
          (static_cast<uint32_t>(c ^ (r & 7)) << 4);
+}
+
+// The address of row i of the warp's rows from the lane that holds it; null: no key.
+__device__ __forceinline__ const uint8_t* row_at(const uint8_t* mine, int i) {
+  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
+}
+
+// Half h of ROWS rows that need no decoding, piece by piece: f(slab, row, piece,
+// address of the piece or null).
+template <int OP, int ROWS, class F>
+__device__ __forceinline__ void each_piece(const uint8_t* mine, int h, int lane, const F& f) {
+  constexpr int kPieces = 8 * Shape<OP>::kHalfSlabs;   // of a row's half: 32 or 16
+  constexpr int kAtOnce = 32 / kPieces;                // rows a warp covers at once
+#pragma unroll
+  for (int i = 0; i < ROWS / kAtOnce; ++i) {
+    const int r = kAtOnce * i + lane / kPieces, c = lane % kPieces;
+    const uint8_t* src = row_at(mine, r);
+    f(Shape<OP>::kHalfSlabs * h + (c >> 3), r, c & 7, src != nullptr ? src + 16 * (kPieces * h + c) : nullptr);
+  }
+  if (h == 0) {
+    constexpr int kPe = 4 * Shape<OP>::kElem;          // pieces of the rotary values: 8 or 4
+#pragma unroll
+    for (int i = 0; i < ROWS * kPe / 32; ++i) {
+      const int r = (32 / kPe) * i + lane / kPe, c = lane % kPe;
+      const uint8_t* src = row_at(mine, r);
+      f(Shape<OP>::kPeSlab, r, c, src != nullptr ? src + 16 * (2 * kPieces + c) : nullptr);
+    }
+  }
 }
 
 // What a lane holds of its warp's eight quantised rows.  Half h of rows 2 j and
@@ -479,11 +585,6 @@ struct Raw {
   uint4 rest[FMT == MLA_CACHE_MX ? 2 : 1];
   uint4 scales;  // mx: the 16 scale bytes of row `lane` (lanes 0..7)
 };
-
-// The address of row i of the warp's eight from the lane that holds it; null: no key.
-__device__ __forceinline__ const uint8_t* row_at(const uint8_t* mine, int i) {
-  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
-}
 
 template <int FMT>
 __device__ __forceinline__ void load_rows(Raw<FMT>& raw, const uint8_t* mine, int lane) {
@@ -509,28 +610,20 @@ __device__ __forceinline__ void load_rows(Raw<FMT>& raw, const uint8_t* mine, in
   }
 }
 
-// Sixteen codes -> two pieces of 16-bit values.
-template <int FMT, bool F16>
+// Sixteen codes -> two pieces of bf16 values.
+template <int FMT>
 __device__ __forceinline__ void decode(const uint4& w, uint32_t byte, uint4& a, uint4& b) {
-  if constexpr (F16) {
-    if (any_nan_code(w)) {
-      codes_to_f16(w, a, b);
-    } else {
-      plain_codes_to_f16(w, a, b);
-    }
+  if ((FMT == MLA_CACHE_MX && byte > kMxPlain) || any_nan_code(w)) {
+    codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_scale(byte) : 1.0f, a, b);
   } else {
-    if ((FMT == MLA_CACHE_MX && byte > kMxPlain) || any_nan_code(w)) {
-      codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_scale(byte) : 1.0f, a, b);
-    } else {
-      plain_codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_mul2(byte) : kBf16Pow120, a, b);
-    }
+    plain_codes_to_bf16(w, FMT == MLA_CACHE_MX ? mx_mul2(byte) : kBf16Pow120, a, b);
   }
 }
 
 // Half h of the warp's rows, decoded, through `put(slab, row, piece, value)`.
 // A lane's two pieces swap places in odd slabs, so that eight lanes' stores
 // fall on different banks.
-template <int FMT, bool F16, class Put>
+template <int FMT, class Put>
 __device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0, int lane, const Put& put) {
   const int slab = 4 * h + ((lane & 15) >> 2), piece = 2 * (lane & 3), odd = (lane >> 2) & 1;
 #pragma unroll
@@ -544,7 +637,7 @@ __device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0,
       byte = (((lane & 8) != 0 ? hi : lo) >> (8 * ((lane >> 1) & 3))) & 0xffu;
     }
     uint4 a, b;
-    decode<FMT, F16>(raw.codes[4 * h + j], byte, a, b);
+    decode<FMT>(raw.codes[4 * h + j], byte, a, b);
     put(slab, r, piece + odd, odd ? b : a);
     put(slab, r, piece + (odd ^ 1), odd ? a : b);
   }
@@ -554,7 +647,7 @@ __device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0,
       for (int i = 0; i < 2; ++i) put(8, row0 + 4 * i + (lane >> 3), lane & 7, raw.rest[i]);
     } else {
       uint4 a, b;
-      decode<FMT, F16>(raw.rest[0], 0u, a, b);
+      decode<FMT>(raw.rest[0], 0u, a, b);
       put(8, row0 + (lane >> 2), 2 * (lane & 3), a);
       put(8, row0 + (lane >> 2), 2 * (lane & 3) + 1, b);
     }
@@ -644,53 +737,53 @@ __device__ __forceinline__ const uint8_t* q_row(const Params& p, int32_t row0, i
 }
 
 // The segment's 64 q rows, by all loader threads; q_full gets one arrival of each.
-template <bool F16>
+template <int FMT, int OP>
 __device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t rows, uint32_t sQ, uint32_t bar, int warp,
                                        int lane) {
+  constexpr int kRows = Roles<FMT, OP>::kRows;
   bool ok;
-  if (p.q_fp8) {
-    const uint8_t* src = q_row(p, row0, rows, 8 * warp + (lane & 7), ok);
-    Raw<MLA_CACHE_E4M3> raw;
-    load_rows<MLA_CACHE_E4M3>(raw, ok && lane < 8 ? src : nullptr, lane);
-    auto put = [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(sQ, s, r, c), v); };
-    store_half<MLA_CACHE_E4M3, F16>(raw, 0, 8 * warp, lane, put);
-    store_half<MLA_CACHE_E4M3, F16>(raw, 1, 8 * warp, lane, put);
+  const uint8_t* mine = q_row(p, row0, rows, kRows * warp + lane % kRows, ok);
+  if (!ok || lane >= kRows) mine = nullptr;
+  if (OP == kBf16 && p.q_fp8) {
+#pragma unroll
+    for (int i = 0; i < kRows / 8; ++i) {
+      const uint8_t* eight = row_at(mine, 8 * i + (lane & 7));
+      Raw<MLA_CACHE_E4M3> raw;
+      load_rows<MLA_CACHE_E4M3>(raw, lane < 8 ? eight : nullptr, lane);
+      auto put = [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(sQ, s, r, c), v); };
+      store_half<MLA_CACHE_E4M3>(raw, 0, kRows * warp + 8 * i, lane, put);
+      store_half<MLA_CACHE_E4M3>(raw, 1, kRows * warp + 8 * i, lane, put);
+    }
     fence_async();
     __syncwarp();
     if (lane == 0) arrive(bar, 32);
-  } else if constexpr (!F16) {
-    // eight lanes to a row: rows 8 warp + lane / 8 and four further on
+  } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * warp + 4 * i + (lane >> 3);
-      const uint8_t* src = q_row(p, row0, rows, r, ok);
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s) cp_async16(piece_addr(sQ, s, r, lane & 7), src + (s * 8 + (lane & 7)) * 16, ok);
-    }
+    for (int h = 0; h < 2; ++h)
+      each_piece<OP, kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+        cp_async16(piece_addr(sQ, s, kRows * warp + r, c), src != nullptr ? src : p.q, src != nullptr);
+      });
     cp_async_arrive(bar);
   }
 }
 
-// Loader warps fill the stages, tile by tile.  kArrive: what one warp's part of
-// a half counts on its barrier.
-template <int FMT, bool F16>
+// Loader warps fill the stages, tile by tile.  A half's barrier counts one
+// arrival a warp, and where rows come by asynchronous copies one a thread too.
+template <int FMT, int OP>
 __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
                                            bool& bad_page) {
-  constexpr bool kCodes = FMT != MLA_CACHE_BF16;
-  constexpr uint32_t kArrive = kCodes ? 1 : 33;
-  const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - kLoadWarp0), lane = static_cast<int>(threadIdx.x) & 31;
-  const int row0 = 8 * warp;
+  using S = Shape<OP>;
+  using R = Roles<FMT, OP>;
+  constexpr bool kDecode = R::kDecode;
+  constexpr uint32_t kArrive = kDecode ? 1 : 33;
+  const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - R::kLoad0), lane = static_cast<int>(threadIdx.x) & 31;
+  const int row0 = R::kRows * warp;
   volatile uint32_t* ab = &sh.abort_flag;
-  // Lane i < 8 looks after row i of the warp's eight: its page number is fetched
-  // two tiles ahead, its row called to L2 one and a half ahead.
+  // Lane i < kRows looks after row i of the warp's: its page number is fetched two tiles ahead.
   TileWalk w;  // two tiles ahead of the one being stored
   KeyAt at;
-  Raw<kCodes ? FMT : MLA_CACHE_E4M3> raw;
-  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, row0 + lane, w.any && lane < 8 && !w.copied); };
-  auto call = [&](const uint8_t* row) {
-    if (row != nullptr)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "n"(row_bytes(FMT)) : "memory");
-  };
+  Raw<kDecode ? FMT : MLA_CACHE_E4M3> raw;
+  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, row0 + lane, w.any && lane < R::kRows && !w.copied); };
   w.start(cur);
   w.next(p, sh);
   Tile now(w);
@@ -699,113 +792,77 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, S
   w.next(p, sh);
   Tile then(w);
   fetch();
-  const uint8_t* next_row = at.address(p, row_bytes(FMT), bad_page);
-  call(next_row);
-  w.next(p, sh);
-  fetch();
-  if constexpr (kCodes) load_rows<FMT>(raw, mine, lane);
-  for (uint32_t it = 0; uniform(now.any ? 1 : 0) != 0; ++it) {
-    const uint32_t st = it & 1u, base = sK + st * kTileBytes, parity = (it / kStages - 1) & 1u;
-    const uint32_t full0 = smem_u32(&sh.bars.kv_full[st][0]), full1 = smem_u32(&sh.bars.kv_full[st][1]);
+  if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
+  uint32_t st = 0, round = 0;  // stage, and how often the stages have been round
+  while (uniform(now.any ? 1 : 0) != 0) {
+    const uint32_t base = sK + st * S::kTile;
     const bool direct = uniform(now.copied ? 0 : 1) != 0;
     const bool first = uniform(now.first ? 1 : 0) != 0;
     const volatile SegmentInfo& info = sh.segments[now.seg & 7];
-    const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * kImageBytes;
-    const bool ok = mine != nullptr;
-    // ---- first half
-    if (it >= kStages && !warp_wait(smem_u32(&sh.bars.kv_empty[st][0]), parity, ab)) return false;
-    if (direct) {
-      if (lane < 8) sh.valid[st][row0 + lane] = ok ? 1 : 0;
-      if constexpr (kCodes) {
-        store_half<FMT, F16>(raw, 0, row0, lane,
-                             [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
-        fence_async();
+    const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * S::kImage;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t full = smem_u32(&sh.bars.kv_full[st][h]);
+      if (round > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st][h]), (round - 1) & 1u, ab)) return false;
+      if (direct) {
+        if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = mine != nullptr ? 1 : 0;
+        if constexpr (kDecode) {
+          store_half<FMT>(raw, h, row0, lane,
+                          [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
+          fence_async();
+        } else {
+          each_piece<OP, R::kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+            cp_async16(piece_addr(base, s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
+          });
+          cp_async_arrive(full);
+        }
         __syncwarp();
-        if (lane == 0) arrive(full0);
+        if (lane == 0) arrive(full);
+      } else if (warp == 0) {
+        if (elect_one()) {
+          constexpr uint32_t kHalf = S::kHalfSlabs * kSlabBytes;
+          if (kArrive > 1) arrive(full, kArrive - 1);
+          arrive_expect(full, kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
+          bulk_copy(base + h * kHalf, image + h * kHalf, kHalf, full);
+          if (h == 0) {
+            bulk_copy(base + S::kPeSlab * kSlabBytes, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
+            bulk_copy(smem_u32(sh.valid[st]), image + S::kTile, kKeys, full);
+          }
+        }
+        __syncwarp();
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint8_t* src = row_at(mine, i);
-          cp_async16(piece_addr(base, lane >> 3, row0 + i, lane & 7), (src != nullptr ? src : p.cache) + 16 * lane, src != nullptr);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const uint8_t* src = row_at(mine, r);
-          cp_async16(piece_addr(base, 8, row0 + r, lane & 7), (src != nullptr ? src : p.cache) + 1024 + 16 * (lane & 7), src != nullptr);
-        }
-        cp_async_arrive(full0);
-        __syncwarp();
-        if (lane == 0) arrive(full0);
+        if (lane == 0) arrive(full, kArrive);
       }
-    } else if (warp == 0) {
-      if (elect_one()) {
-        if (kArrive > 1) arrive(full0, kArrive - 1);
-        arrive_expect(full0, 5 * kSlabBytes + kKeys);
-        bulk_copy(base, image, 4 * kSlabBytes, full0);
-        bulk_copy(base + 8 * kSlabBytes, image + 8 * kSlabBytes, kSlabBytes, full0);
-        bulk_copy(smem_u32(sh.valid[st]), image + kTileBytes, kKeys, full0);
+      if (h == 0 && first) {
+        // the segment's q rows, once the previous segment's scores have been computed
+        if (now.seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
+        load_q<FMT, OP>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
       }
-      __syncwarp();
-    } else {
-      if (lane == 0) arrive(full0, kArrive);
-    }
-    if (first) {
-      // the segment's q rows, once the previous segment's scores have been computed
-      if (now.seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
-      load_q<F16>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
-    }
-    // ---- second half
-    if (it >= kStages && !warp_wait(smem_u32(&sh.bars.kv_empty[st][1]), parity, ab)) return false;
-    if (direct) {
-      if constexpr (kCodes) {
-        store_half<FMT, F16>(raw, 1, row0, lane,
-                             [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
-        fence_async();
-        __syncwarp();
-        if (lane == 0) arrive(full1);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint8_t* src = row_at(mine, i);
-          cp_async16(piece_addr(base, 4 + (lane >> 3), row0 + i, lane & 7), (src != nullptr ? src : p.cache) + 512 + 16 * lane, src != nullptr);
-        }
-        cp_async_arrive(full1);
-        __syncwarp();
-        if (lane == 0) arrive(full1);
-      }
-    } else if (warp == 0) {
-      if (elect_one()) {
-        if (kArrive > 1) arrive(full1, kArrive - 1);
-        arrive_expect(full1, 4 * kSlabBytes);
-        bulk_copy(base + 4 * kSlabBytes, image + 4 * kSlabBytes, 4 * kSlabBytes, full1);
-      }
-      __syncwarp();
-    } else {
-      if (lane == 0) arrive(full1, kArrive);
     }
     // the next tile's loads go out behind the fences, which would wait for them
-    mine = next_row;
-    if constexpr (kCodes) load_rows<FMT>(raw, mine, lane);
-    next_row = at.address(p, row_bytes(FMT), bad_page);
-    call(next_row);
+    mine = at.address(p, row_bytes(FMT), bad_page);
+    if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
     now = then;
-    then = Tile(w);
     w.next(p, sh);
+    then = Tile(w);
     fetch();
+    if (++st == S::kStages) {
+      st = 0;
+      ++round;
+    }
   }
   return true;
 }
 
-template <int FMT, bool F16>
+template <int FMT, int OP>
 __device__ __forceinline__ void loader(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK) {
   bool bad_page = false;
-  const bool good = load_tiles<FMT, F16>(p, cur, sh, sQ, sK, bad_page);
+  const bool good = load_tiles<FMT, OP>(p, cur, sh, sQ, sK, bad_page);
   // no copy may be under way when the CTA ends: on the way out after a timeout
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!good) {
-    for (int i = 0; i < 2 * kStages; ++i)
+    for (int i = 0; i < 2 * Shape<OP>::kStages; ++i)
       for (uint32_t parity = 0; parity < 2; ++parity)
         (void)warp_wait(smem_u32(&sh.bars.kv_full[i >> 1][i & 1]), parity, &sh.never);
   }
@@ -817,48 +874,61 @@ __device__ __forceinline__ void loader(const Params& p, const Cursor& cur, Share
 }
 
 // The products of one tile's weights with its values, into the sums: columns 0..255, then 256..511.
-template <bool F16, bool FIRST>
+template <int OP, bool FIRST>
 __device__ __forceinline__ void pv_half(uint64_t p, uint64_t v, uint32_t tmem, int half) {
-  constexpr uint32_t id = instr_desc(F16, 256, true);
+  using S = Shape<OP>;
+  constexpr uint32_t id = instr_desc<OP>(256, true);
+  constexpr uint64_t kStep = static_cast<uint64_t>(kSlabBytes / S::kKeySteps) >> 4;  // that many keys further down the tile
   const uint32_t d = tmem + static_cast<uint32_t>(half) * 128u;
-  const uint64_t vh = v + static_cast<uint64_t>(half * kHalfSlabs * (kSlabBytes >> 4));
-  mma_ws<!FIRST>(d, p, vh, id);
+  const uint64_t vh = v + static_cast<uint64_t>(half * S::kHalfSlabs * (kSlabBytes >> 4));
 #pragma unroll
-  for (int j = 1; j < kKeys / 16; ++j)
-    mma_ws<true>(d, p + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j * 128), id);
-}
-
-template <bool F16, bool FIRST>
-__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st) {
-  pv_half<F16, FIRST>(p, v, tmem, 0);
-  commit(smem_u32(&sh.bars.kv_empty[st][0]));
-  pv_half<F16, FIRST>(p, v, tmem, 1);
-  commit(smem_u32(&sh.bars.kv_empty[st][1]));
-  commit(smem_u32(&sh.bars.pv_done));
-}
-
-// Scores from slab S0 on, N of them (four steps of 16 each); slab 8 counts as the first half's first.
-template <bool F16, int S0, int N, bool FIRST>
-__device__ __forceinline__ void qk_slabs(uint64_t q, uint64_t k, uint32_t d) {
-  constexpr uint32_t id = instr_desc(F16, kKeys, false);
+  for (int t = 0; t < S::kTerms; ++t) {
+    // weights: 32-byte steps along a row; kF8 terms at bytes 0 and 64 of the first slab, 0 of the second
+    const uint64_t pt = p + static_cast<uint64_t>(t == 1 ? 4 : t == 2 ? kSlabBytes >> 4 : 0);
 #pragma unroll
-  for (int j = 0; j < 4 * N; ++j) {
-    const uint64_t off = static_cast<uint64_t>((S0 + (j >> 2)) * (kSlabBytes >> 4) + (j & 3) * 2);
-    if (FIRST && j == 0) {
-      mma_ws<false>(d, q + off, k + off, id);
-    } else {
-      mma_ws<true>(d, q + off, k + off, id);
+    for (int j = 0; j < S::kKeySteps; ++j) {
+      if (FIRST && t == 0 && j == 0) {
+        mma_ws<OP, false>(d, pt, vh, id);
+      } else {
+        mma_ws<OP, true>(d, pt + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j) * kStep, id);
+      }
     }
   }
 }
 
-template <bool F16>
+template <int OP, bool FIRST>
+__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st) {
+  pv_half<OP, FIRST>(p, v, tmem, 0);
+  commit(smem_u32(&sh.bars.kv_empty[st][0]));
+  pv_half<OP, FIRST>(p, v, tmem, 1);
+  commit(smem_u32(&sh.bars.kv_empty[st][1]));
+  commit(smem_u32(&sh.bars.pv_done));
+}
+
+// Scores: MMAs over STEPS 32-byte pieces of the rows from slab S0 on.
+template <int OP, int S0, int STEPS, bool FIRST>
+__device__ __forceinline__ void qk_slabs(uint64_t q, uint64_t k, uint32_t d) {
+  constexpr uint32_t id = instr_desc<OP>(kKeys, false);
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const uint64_t off = static_cast<uint64_t>((S0 + (j >> 2)) * (kSlabBytes >> 4) + (j & 3) * 2);
+    if (FIRST && j == 0) {
+      mma_ws<OP, false>(d, q + off, k + off, id);
+    } else {
+      mma_ws<OP, true>(d, q + off, k + off, id);
+    }
+  }
+}
+
+template <int OP>
 __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK, uint32_t sP,
                                          uint32_t tmem) {
+  using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
   const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
   uint32_t s = 0, v = 0;        // the next tile to get scores, and sums: v <= s <= v + 2
+  uint32_t s_st = 0, s_round = 0, v_st = 0;  // their stages, s's round
   bool begun = false;           // tile s has its first half's scores
   uint32_t seg = 0;             // segments begun
   int left = 0;                 // tiles of the current segment without scores
@@ -878,46 +948,57 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
       if (more) ++seg;
     }
     if (left == 0 && v == s) break;
-    if (v < s && warp_test(smem_u32(&sh.bars.p_full), v & 1u)) {
-      const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
-      if (!opens || v_seg == 0 || warp_test(smem_u32(&sh.bars.o_empty), (v_seg - 1) & 1u)) {
-        fence_after();
-        const uint64_t vd = dV + (v & 1u) * (kTileBytes >> 4);
-        if (opens) {
-          pv_products<F16, true>(sh, dP, vd, tmem, v & 1u);
-          ++v_seg;
-        } else {
-          pv_products<F16, false>(sh, dP, vd, tmem, v & 1u);
-        }
-        ++v;
-        idle = 0;
-        continue;
-      }
-    }
-    const uint32_t st = s & 1u, full = (s / kStages) & 1u, d = tmem + kTmemS + 32u * st;
-    const uint64_t k = dK + st * (kTileBytes >> 4);
-    if (left > 0 && !begun && s < v + 2 && warp_test(smem_u32(&sh.bars.kv_full[st][0]), full) &&
-        (!first || warp_test(smem_u32(&sh.bars.q_full), (seg - 1) & 1u)) &&
-        (s < 2 || warp_test(smem_u32(&sh.bars.s_empty[st]), (s / 2 - 1) & 1u))) {
-      fence_async();  // rows that came by plain asynchronous copies, before the tensor cores read them
+    const uint32_t s_buf = s & 1u;
+    const uint32_t got = __reduce_or_sync(
+        0xffffffffu, ask(smem_u32(&sh.bars.p_full), v & 1u, 0) | ask(smem_u32(&sh.bars.o_empty), (v_seg - 1) & 1u, 1) |
+                         ask(smem_u32(&sh.bars.kv_full[s_st][0]), s_round & 1u, 2) |
+                         ask(smem_u32(&sh.bars.kv_full[s_st][1]), s_round & 1u, 3) |
+                         ask(smem_u32(&sh.bars.q_full), (seg - 1) & 1u, 4) |
+                         ask(smem_u32(&sh.bars.s_empty[s_buf]), (s / 2 - 1) & 1u, 5));
+    const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
+    if (v < s && (got & 1u) != 0u && (!opens || v_seg == 0 || (got & 2u) != 0u)) {
       fence_after();
-      qk_slabs<F16, 8, 1, true>(dQ, k, d);
-      qk_slabs<F16, 0, kHalfSlabs, false>(dQ, k, d);
-      begun = true;
+      const uint64_t vd = dV + v_st * (S::kTile >> 4);
+      if (opens) {
+        pv_products<OP, true>(sh, dP, vd, tmem, v_st);
+        ++v_seg;
+      } else {
+        pv_products<OP, false>(sh, dP, vd, tmem, v_st);
+      }
+      ++v;
+      v_st = v_st + 1 == S::kStages ? 0 : v_st + 1;
       idle = 0;
       continue;
     }
-    if (begun && warp_test(smem_u32(&sh.bars.kv_full[st][1]), full)) {
+    const uint32_t d = tmem + kTmemS + 32u * s_buf;
+    const uint64_t k = dK + s_st * (S::kTile >> 4);
+    bool went = false;
+    if (left > 0 && !begun && s < v + 2 && (got & 4u) != 0u && (!first || (got & 16u) != 0u) &&
+        (s < 2 || (got & 32u) != 0u)) {
+      fence_async();  // rows that came by plain asynchronous copies, before the tensor cores read them
+      fence_after();
+      qk_slabs<OP, S::kPeSlab, S::kPeSteps, true>(dQ, k, d);
+      qk_slabs<OP, 0, 4 * S::kHalfSlabs, false>(dQ, k, d);
+      begun = went = true;
+    }
+    if (begun && (got & 8u) != 0u) {
       fence_async();
       fence_after();
-      qk_slabs<F16, kHalfSlabs, kHalfSlabs, false>(dQ, k, d);
-      commit(smem_u32(&sh.bars.s_full[st]));
+      qk_slabs<OP, S::kHalfSlabs, 4 * S::kHalfSlabs, false>(dQ, k, d);
+      commit(smem_u32(&sh.bars.s_full[s_buf]));
       --left;
       if (left == 0) commit(smem_u32(&sh.bars.q_empty));
-      first_bits = (first_bits & ~(1u << st)) | ((first ? 1u : 0u) << st);
+      first_bits = (first_bits & ~(1u << s_buf)) | ((first ? 1u : 0u) << s_buf);
       first = false;
       begun = false;
+      went = true;
       ++s;
+      if (++s_st == S::kStages) {
+        s_st = 0;
+        ++s_round;
+      }
+    }
+    if (went) {
       idle = 0;
       continue;
     }
@@ -934,73 +1015,98 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
   (void)warp_wait(smem_u32(&sh.bars.drained), 0u, &sh.never);
 }
 
-template <bool F16>
+// The softmax of WARPS warps.  A thread has one row (TMEM lane), and of a tile's
+// scores half `half` of the keys, of that (8 warps) half `sub`; of the sums the
+// same half of each 256 columns and half `sub` of the TMEM columns.
+template <int OP, int WARPS>
 __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared& sh, uint32_t sP, uint32_t tmem,
                                              float scale2) {
+  constexpr int kN = 32 * 4 / WARPS;           // keys of a thread: 32 or 16
+  constexpr int kParts = WARPS / 2;            // threads to a row
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const int r = (warp & 1) * 32 + lane;  // this thread's row
-  const int half = warp >> 1;            // its half of the keys (scores) and of each 256 columns (sums)
-  const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+  const int r = (warp & 1) * 32 + lane;
+  const int half = (warp >> 1) & 1, sub = warp >> 2;
+  const int part = half * (kParts / 2) + sub;  // keys part * kN ..
+  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
   const bool negative = scale2 < 0.0f;  // then the scores change sign, and the scale
   scale2 = fabsf(scale2);
   volatile uint32_t* ab = &sh.abort_flag;
   Segment seg;
-  uint32_t it = 0;
+  uint32_t it = 0, st = 0, round = 0;
   bool good = true;
   while (good && next_segment(p, cur, seg)) {
     float m = -INFINITY;  // the reference maximum of the row, in powers of two
     float l = 0.0f;       // this thread's share of the denominator
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
-      const uint32_t st = it & 1u;
-      good = warp_wait(smem_u32(&sh.bars.s_full[st]), (it / 2) & 1u, ab) && good;
+      const uint32_t buf = it & 1u;
+      good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab) && good;
       // complete by now; the flags may have come through it by the copy engine
-      good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), (it / kStages) & 1u, ab) && good;
+      good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab) && good;
       fence_after();
-      uint32_t v[32];
-      tmem_ld32(tmem + kTmemS + 32u * st + lanes, v);
-      const uint4 va = ld_shared(smem_u32(&sh.valid[st][32 * half])), vb = ld_shared(smem_u32(&sh.valid[st][32 * half + 16]));
+      uint32_t v[kN];
+      tmem_ld<kN>(tmem + kTmemS + 32u * buf + lanes + static_cast<uint32_t>(sub * kN), v);
+      uint32_t ok[kN / 4];
+#pragma unroll
+      for (int j = 0; j < kN / 16; ++j) {
+        const uint4 f = ld_shared(smem_u32(&sh.valid[st][part * kN + 16 * j]));
+        ok[4 * j] = f.x;
+        ok[4 * j + 1] = f.y;
+        ok[4 * j + 2] = f.z;
+        ok[4 * j + 3] = f.w;
+      }
       fence_before();
       __syncwarp();
-      if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[st]));
+      if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[buf]));
+      if (++st == Shape<OP>::kStages) {
+        st = 0;
+        ++round;
+      }
       if (negative) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] ^= 0x80000000u;
+        for (int j = 0; j < kN; ++j) v[j] ^= 0x80000000u;
       }
-      const bool whole = (va.x & va.y & va.z & va.w & vb.x & vb.y & vb.z & vb.w) == 0x01010101u;
-      const uint32_t ok[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+      uint32_t all = ok[0];
+#pragma unroll
+      for (int j = 1; j < kN / 4; ++j) all &= ok[j];
+      const bool whole = all == 0x01010101u;
       if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? v[j] : 0xff800000u;
+        for (int j = 0; j < kN; ++j) v[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? v[j] : 0xff800000u;
       }
-      float t[8];
+      float t[kN / 4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        t[j] = fmaxf(fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 8])),
-                     fmaxf(__uint_as_float(v[j + 16]), __uint_as_float(v[j + 24])));
-      const float raw = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-      const float top = raw == -INFINITY ? -INFINITY : raw * scale2;  // scale2 >= 0: the largest score
+      for (int j = 0; j < kN / 4; ++j)
+        t[j] = fmaxf(fmaxf(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])),
+                     fmaxf(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])));
+#pragma unroll
+      for (int n = kN / 8; n > 0; n /= 2)
+#pragma unroll
+        for (int j = 0; j < n; ++j) t[j] = fmaxf(t[j], t[j + n]);
+      const float top = t[0] == -INFINITY ? -INFINITY : t[0] * scale2;  // scale2 >= 0: the largest score
       const bool first = kt == seg.k0;
       // One vote a tile: whether a row's reference must move, or a wait ran out
-      // (then all four warps leave together).
-      const bool moved = bar_or(1, 32 * kSoftWarps, first || top > m + kRescale || !good);
+      // (then all the warps leave together).
+      const bool moved = bar_or(1, 32 * WARPS, first || top > m + kRescale || !good);
       float factor = 1.0f;
       if (moved) {
-        if (bar_or(2, 32 * kSoftWarps, !good)) {
+        if (bar_or(2, 32 * WARPS, !good)) {
           good = false;
           break;
         }
-        sh.xch[half][r] = top;
-        bar_sync(2, 32 * kSoftWarps);
-        const float next = fmaxf(m, fmaxf(top, sh.xch[half ^ 1][r]));
+        sh.xch[part][r] = top;
+        bar_sync(2, 32 * WARPS);
+        float next = m;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) next = fmaxf(next, sh.xch[i][r]);
         if (!first && next > m) factor = m == -INFINITY ? 0.0f : exp2_fast(m - next);
         m = next;
         l *= factor;
       }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      uint32_t w[16];
+      const float ref = (m == -INFINITY ? 0.0f : m) - (OP == kF8 ? kF8Lift : 0.0f);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint32_t w[kN / 2], mid[kN / 4], lo[kN / 4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < kN / 2; ++j) {
         float a = exp2_fast(fmaf(__uint_as_float(v[2 * j]), scale2, -ref));
         float b = exp2_fast(fmaf(__uint_as_float(v[2 * j + 1]), scale2, -ref));
         if (!whole) {  // (a zero scale makes no weight of a masked score)
@@ -1008,32 +1114,56 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
           b = (ok[j >> 1] >> (16 * (j & 1) + 8)) & 1u ? b : 0.0f;
         }
         sum[j & 3] += a + b;
-        if constexpr (F16) {
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(b), "f"(a));
+        if constexpr (OP == kF8) {
+          uint32_t h, x;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+          // each remainder is exact in fp16: it has the bits the term left over
+          const uint32_t t0 = e5m2x2(h), r0 = sub_f16x2(h, e5m2x2_to_f16x2(t0));
+          const uint32_t t1 = e5m2x2(r0), r1 = sub_f16x2(r0, e5m2x2_to_f16x2(t1));
+          x = e5m2x2(r1);
+          if ((j & 1) == 0) {
+            w[j >> 1] = t0;
+            mid[j >> 1] = t1;
+            lo[j >> 1] = x;
+          } else {
+            w[j >> 1] |= t0 << 16;
+            mid[j >> 1] |= t1 << 16;
+            lo[j >> 1] |= x << 16;
+          }
         } else {
           w[j] = pack_bf16x2(a, b);
         }
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (it > 0) {  // the previous tile's weights have been read, its products are in the sums
+      if (it > 0)  // the previous tile's weights have been read, its products are in the sums
         good = warp_wait(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
-      }
       if (good && moved && !first) {
         fence_after();
 #pragma unroll 1
-        for (uint32_t c = 0; c < 256; c += 32) {
-          tmem_ld32(tmem + lanes + c, v);
+        for (uint32_t c = 0; c < 1024u / WARPS; c += 32) {
+          uint32_t o[32];
+          const uint32_t at = tmem + lanes + static_cast<uint32_t>(sub) * 128u + c;
+          tmem_ld<32>(at, o);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
-          tmem_st32(tmem + lanes + c, v);
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
+          tmem_st32(at, o);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
+      if constexpr (OP == kF8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        st_shared(sP + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>((half * 4 + j) ^ (r & 7)) << 4),
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (int j = 0; j < kN / 16; ++j) {
+          const int c = part * (kN / 16) + j;
+          st_shared(piece_addr(sP, 0, r, c), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+          st_shared(piece_addr(sP, 0, r, 4 + c), make_uint4(mid[4 * j], mid[4 * j + 1], mid[4 * j + 2], mid[4 * j + 3]));
+          st_shared(piece_addr(sP, 1, r, c), make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN / 8; ++j)
+          st_shared(piece_addr(sP, 0, r, part * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+      }
+      fence_async();
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.p_full));
@@ -1041,7 +1171,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     if (!good) break;
     // ---- the segment's result
     good = warp_wait(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
-    if (bar_or(1, 32 * kSoftWarps, !good)) {
+    if (bar_or(1, 32 * WARPS, !good)) {
       good = false;
       break;
     }
@@ -1049,9 +1179,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     const bool keep = r < seg.rows;
     uint4* dst = reinterpret_cast<uint4*>(seg.part) + r;
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 32) {
+    for (int i = 0; i < 1024 / WARPS; i += 32) {
+      const int c = sub * 128 + i;
       uint32_t v[32];
-      tmem_ld32(tmem + lanes + static_cast<uint32_t>(c), v);
+      tmem_ld<32>(tmem + lanes + static_cast<uint32_t>(c), v);
       // TMEM column c of this lane: output column (c / 128) 256 + half 128 + c % 128
       const int chunk0 = ((c >> 7) * 256 + half * 128 + (c & 127)) / 4;
       if (keep) {
@@ -1064,14 +1195,17 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     fence_before();
     __syncwarp();
     if (lane == 0) arrive(smem_u32(&sh.bars.o_empty));
-    sh.xch[half][r] = l;
-    bar_sync(2, 32 * kSoftWarps);
-    if (half == 0 && keep) {
+    sh.xch[part][r] = l;
+    bar_sync(2, 32 * WARPS);
+    if (part == 0 && keep) {
       float* stat = reinterpret_cast<float*>(seg.part + static_cast<int64_t>(seg.part_rows) * kChunks * 16);
-      __stcg(stat + r, m);
-      __stcg(stat + seg.part_rows + r, l + sh.xch[1][r]);
+      float den = l;
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) den += sh.xch[i][r];
+      __stcg(stat + r, OP == kF8 ? (m == -INFINITY ? m : m - kF8Lift) : m);
+      __stcg(stat + seg.part_rows + r, den);
     }
-    bar_sync(2, 32 * kSoftWarps);
+    bar_sync(2, 32 * WARPS);
   }
   if (!good && *ab == 0u && lane == 0) {
     *ab = 1u;
@@ -1109,7 +1243,7 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
     total += sh.warp_sum[w];
   }
   // at least a tile's cost, so that every CTA between a row tile's first and last has one of its key tiles
-  const int64_t least = p.tile_cost > kCostImage ? p.tile_cost : kCostImage;
+  const int64_t least = p.tile_cost > p.image_cost ? p.tile_cost : p.image_cost;
   const int64_t each = (total + p.ctas - 1) / p.ctas > least ? (total + p.ctas - 1) / p.ctas : least;
   Cursor c;
   c.pos = each * blockIdx.x;
@@ -1135,17 +1269,19 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   return c;
 }
 
-template <int FMT, bool F16>
+template <int FMT, int OP>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
-  // a half of a tile: one arrival a warp, or one a thread and one a warp
-  constexpr uint32_t kFill = FMT == MLA_CACHE_BF16 ? 33 * kLoadWarps : kLoadWarps;
+  using S = Shape<OP>;
+  using R = Roles<FMT, OP>;
+  // a half of a tile: one arrival a loader warp, and one a thread where rows come by asynchronous copies
+  constexpr uint32_t kFill = (R::kDecode ? 1 : 33) * R::kLoad;
   extern __shared__ uint8_t dsmem[];
   __shared__ Shared sh;
   const int warp = uniform(static_cast<int>(threadIdx.x) >> 5);
   const uint32_t sQ = (smem_u32(dsmem) + 1023u) & ~1023u;
-  const uint32_t sK = sQ + kTileBytes;
-  const uint32_t sP = sK + kStages * kTileBytes;
-  if (warp == kMmaWarp) {
+  const uint32_t sK = sQ + S::kTile;
+  const uint32_t sP = sK + S::kStages * S::kTile;
+  if (warp == R::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -1159,19 +1295,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
     auto init = [](uint64_t* b, uint32_t n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       for (int h = 0; h < 2; ++h) {
         init(&sh.bars.kv_full[i][h], kFill);
         init(&sh.bars.kv_empty[i][h], 1);
       }
-      init(&sh.bars.s_full[i], 1);
-      init(&sh.bars.s_empty[i], kSoftWarps);
     }
-    init(&sh.bars.q_full, 32 * kLoadWarps);
+    for (int i = 0; i < 2; ++i) {
+      init(&sh.bars.s_full[i], 1);
+      init(&sh.bars.s_empty[i], R::kSoft);
+    }
+    init(&sh.bars.q_full, 32 * R::kLoad);
     init(&sh.bars.q_empty, 1);
-    init(&sh.bars.p_full, kSoftWarps);
+    init(&sh.bars.p_full, R::kSoft);
     init(&sh.bars.pv_done, 1);
-    init(&sh.bars.o_empty, kSoftWarps);
+    init(&sh.bars.o_empty, R::kSoft);
     init(&sh.bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1183,20 +1321,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(sh.tmem)));
   const Cursor cur = plan_run(p, sh);
   if (uniform(cur.pos < cur.end ? 1 : 0) != 0) {  // a branch that the compiler sees is uniform
-    if (warp < kSoftWarps) {
+    if (warp < R::kSoft) {
       float scale2 = p.sm_scale * 1.4426950408889634f;  // powers of two: log2(e)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
-      softmax_role<F16>(p, cur, sh, sP, tmem, scale2);
-    } else if (warp == kMmaWarp) {
-      mma_role<F16>(p, cur, sh, sQ, sK, sP, tmem);
+      softmax_role<OP, R::kSoft>(p, cur, sh, sP, tmem, scale2);
+    } else if (warp == R::kMma) {
+      mma_role<OP>(p, cur, sh, sQ, sK, sP, tmem);
     } else {
-      loader<FMT, F16>(p, cur, sh, sQ, sK);
+      loader<FMT, OP>(p, cur, sh, sQ, sK);
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == R::kMma) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
@@ -1209,7 +1347,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
 // values, zeros where there is no key, and a flag for each key); the attention
 // kernel then fetches a tile half with two or three bulk copies.  One block a
 // tile; blocks behind a prefix's end leave.
-template <int FMT, bool F16>
+template <int FMT, int OP>
 __global__ void __launch_bounds__(256) image_kernel(const Params p) {
   pdl_wait();
   const int64_t g = blockIdx.y;
@@ -1219,7 +1357,7 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
   if (kt < x.key_tiles() && x.rows > 0) {
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     const int row0 = 8 * warp;
-    uint8_t* dst = p.image + (g * p.image_tiles + kt) * kImageBytes;
+    uint8_t* dst = p.image + (g * p.image_tiles + kt) * Shape<OP>::kImage;
     KeyAt at;
     bool bad_page = false;
     at.fetch(p, x.table, static_cast<int32_t>(x.len), static_cast<int32_t>(kt), row0 + lane, lane < 8);
@@ -1227,34 +1365,19 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
     auto put = [&](int s, int r, int c, const uint4& v) {
       *reinterpret_cast<uint4*>(dst + piece_addr(0, s, r, c)) = v;
     };
-    if constexpr (FMT == MLA_CACHE_BF16) {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 v[18];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4* src = reinterpret_cast<const uint4*>(row_at(mine, i));
-        v[2 * i] = src != nullptr ? __ldcg(src + lane) : zero;
-        v[2 * i + 1] = src != nullptr ? __ldcg(src + 32 + lane) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4* src = reinterpret_cast<const uint4*>(row_at(mine, 4 * i + (lane >> 3)));
-        v[16 + i] = src != nullptr ? __ldcg(src + 64 + (lane & 7)) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        put(lane >> 3, row0 + i, lane & 7, v[2 * i]);
-        put(4 + (lane >> 3), row0 + i, lane & 7, v[2 * i + 1]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) put(8, row0 + 4 * i + (lane >> 3), lane & 7, v[16 + i]);
-    } else {
+    if constexpr (Roles<FMT, OP>::kDecode) {
       Raw<FMT> raw;
       load_rows<FMT>(raw, mine, lane);
-      store_half<FMT, F16>(raw, 0, row0, lane, put);
-      store_half<FMT, F16>(raw, 1, row0, lane, put);
+      store_half<FMT>(raw, 0, row0, lane, put);
+      store_half<FMT>(raw, 1, row0, lane, put);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        each_piece<OP, 8>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+          put(s, row0 + r, c, src != nullptr ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0));
+        });
     }
-    if (lane < 8) dst[kTileBytes + row0 + lane] = mine != nullptr ? 1 : 0;
+    if (lane < 8) dst[Shape<OP>::kTile + row0 + lane] = mine != nullptr ? 1 : 0;
     if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
   }
   pdl_trigger();
@@ -1441,7 +1564,9 @@ struct Layout {
   int64_t prefix_part, own_part, image, image_tiles, bytes;
 };
 
+// (The bf16 image's size: the caller need not know which operands a call takes.)
 Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t ctas) {
+  constexpr int64_t kImageBytes = Shape<kBf16>::kImage;
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout l;
   l.prefix_part = up(8 * (1 + G + T));
@@ -1455,15 +1580,23 @@ Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t c
   return l;
 }
 
-template <int FMT, bool F16>
-const void* kernel_for() {
-  return reinterpret_cast<const void*>(&attend_kernel<FMT, F16>);
+// The kernels of a call: by format, and with both q and cache in e4m3 on the codes themselves.
+struct Kernels {
+  const void* attend;
+  const void* image;
+  uint32_t smem;
+  int32_t image_bytes, tile_cost, image_cost;
+};
+
+template <int FMT, int OP>
+Kernels kernels_of(int32_t tile_cost) {
+  return Kernels{reinterpret_cast<const void*>(&attend_kernel<FMT, OP>),
+                 reinterpret_cast<const void*>(&image_kernel<FMT, OP>), Shape<OP>::kSmem,
+                 static_cast<int32_t>(Shape<OP>::kImage), tile_cost, OP == kF8 ? kCostF8 : kCostImage};
 }
 
-template <int FMT, bool F16>
-const void* image_for() {
-  return reinterpret_cast<const void*>(&image_kernel<FMT, F16>);
-}
+const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kernels_of<MLA_CACHE_E4M3, kBf16>(kCostCodes),
+                             kernels_of<MLA_CACHE_MX, kBf16>(kCostCodes), kernels_of<MLA_CACHE_E4M3, kF8>(kCostF8)};
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
@@ -1582,30 +1715,29 @@ mla_status mla_prefix_attend_launch(
   p.own_part = ws + lay.own_part;
   p.own_rows = static_cast<int32_t>(H < kRowsTile ? H : kRowsTile);
   p.ctas = sms;
-  p.tile_cost = format == MLA_CACHE_BF16 ? kCostRows : kCostCodes;
   p.status = status;
 
-  static const void* const kernels[4] = {kernel_for<MLA_CACHE_BF16, false>(), kernel_for<MLA_CACHE_E4M3, false>(),
-                                         kernel_for<MLA_CACHE_MX, false>(), kernel_for<MLA_CACHE_E4M3, true>()};
   const int k = format == MLA_CACHE_E4M3 && q8 ? 3 : format;
+  const Kernels& ks = kKernels[k];
+  p.image_bytes = ks.image_bytes;
+  p.tile_cost = ks.tile_cost;
+  p.image_cost = ks.image_cost;
   if (!g_smem_ready[dev][k].load(std::memory_order_acquire)) {
     // idempotent: two threads racing here both set the same attribute
     const cudaError_t e =
-        cudaFuncSetAttribute(kernels[k], cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+        cudaFuncSetAttribute(ks.attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ks.smem));
     if (e != cudaSuccess) return mla::cuda_failure(e);
     g_smem_ready[dev][k].store(true, std::memory_order_release);
   }
   void* args[] = {&p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;
   if (p.image != nullptr) {
-    static const void* const images[4] = {image_for<MLA_CACHE_BF16, false>(), image_for<MLA_CACHE_E4M3, false>(),
-                                          image_for<MLA_CACHE_MX, false>(), image_for<MLA_CACHE_E4M3, true>()};
-    s = launch(images[k], dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
+    s = launch(ks.image, dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
                args);
     if (s != MLA_OK) return s;
     pdl = true;
   }
-  s = launch(kernels[k], dim3(static_cast<unsigned>(sms), 1, 1), kThreads, kSmemBytes, pdl, stream, args);
+  s = launch(ks.attend, dim3(static_cast<unsigned>(sms), 1, 1), kThreads, ks.smem, pdl, stream, args);
   if (s != MLA_OK) return s;
 
   // slices: enough blocks for every SM to have some, a thread not below one chunk of columns
