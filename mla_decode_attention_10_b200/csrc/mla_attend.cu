@@ -37,6 +37,8 @@
 // Every wait is bounded: on timeout a status bit is set, all roles stop, TMEM
 // is freed and the kernel returns.
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -133,6 +135,7 @@ struct Params {
   int32_t own_rows;   // rows of an own segment: min(H, 64)
   int32_t ctas;       // CTAs of the attention kernel
   int32_t image_bytes;  // of one tile's image
+  int32_t box_rows;     // cache rows of one tensor copy (8, 16, 32 or 64), or 0: none are made
   int32_t tile_cost, image_cost;  // of a tile read from the cache, from an image
   int32_t* status;
 };
@@ -406,22 +409,43 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Whether the phase of `parity` has completed, as bit `bit`, in the lane that
-// asks.  One lane asks (32 lanes' asking costs 32 times as much of the
-// shared-memory pipe); the MMA warp asks for all it might need at once and
-// joins the answers with one reduction, so that a round costs one trip.
-__device__ __forceinline__ uint32_t ask(uint32_t bar, uint32_t parity, int bit) {
-  uint32_t done;
+// Which of six phases have completed, as bits.  One lane asks (32 lanes' asking
+// costs 32 times as much of the shared-memory pipe) for all six at once, so that
+// a round of the MMA warp costs one trip to shared memory.
+__device__ __forceinline__ uint32_t ask(const uint32_t (&bar)[6], const uint32_t (&parity)[6]) {
+  uint32_t bits;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, 0, 0;\n\t"
+      "{\n\t.reg .pred q, p0, p1, p2, p3, p4, p5;\n\t"
+      ".reg .b32 a, b, c;\n\t"
+      "setp.ne.b32 p0, 0, 0;\n\t"
+      "setp.ne.b32 p1, 0, 0;\n\t"
+      "setp.ne.b32 p2, 0, 0;\n\t"
+      "setp.ne.b32 p3, 0, 0;\n\t"
+      "setp.ne.b32 p4, 0, 0;\n\t"
+      "setp.ne.b32 p5, 0, 0;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p0, [%1], %7;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p1, [%2], %8;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p2, [%3], %9;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p3, [%4], %10;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p4, [%5], %11;\n\t"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p5, [%6], %12;\n\t"
+      "selp.u32 a, 1, 0, p0;\n\t"
+      "selp.u32 b, 2, 0, p1;\n\t"
+      "or.b32 a, a, b;\n\t"
+      "selp.u32 b, 4, 0, p2;\n\t"
+      "selp.u32 c, 8, 0, p3;\n\t"
+      "or.b32 b, b, c;\n\t"
+      "or.b32 a, a, b;\n\t"
+      "selp.u32 b, 16, 0, p4;\n\t"
+      "selp.u32 c, 32, 0, p5;\n\t"
+      "or.b32 b, b, c;\n\t"
+      "or.b32 %0, a, b;\n\t}"
+      : "=r"(bits)
+      : "r"(bar[0]), "r"(bar[1]), "r"(bar[2]), "r"(bar[3]), "r"(bar[4]), "r"(bar[5]), "r"(parity[0]), "r"(parity[1]),
+        "r"(parity[2]), "r"(parity[3]), "r"(parity[4]), "r"(parity[5])
       : "memory");
-  return done << bit;
+  return __reduce_or_sync(0xffffffffu, bits);
 }
 
 // Waits for the phase, at most kWaitSpins tries or until another role gave up.
@@ -505,6 +529,15 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+// A box of the cache (128 bytes of `box_rows` rows) into swizzled rows, counted on the barrier.
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
@@ -668,7 +701,7 @@ struct TileWalk {
 
   __device__ __forceinline__ void start(const Cursor& c) {
     cur = c;
-    kt = k1 = seg = 0;
+    kt = k1 = seg = len = 0;
     copied = first = false;
     any = true;
   }
@@ -697,10 +730,10 @@ struct TileWalk {
 
 struct Tile {
   int32_t kt, seg;
-  bool copied, first, any;
+  bool copied, first, any, whole;  // whole: no key behind the sequence's end
 
   __device__ __forceinline__ explicit Tile(const TileWalk& w)
-      : kt(w.kt), seg(w.seg), copied(w.copied), first(w.first), any(w.any) {}
+      : kt(w.kt), seg(w.seg), copied(w.copied), first(w.first), any(w.any), whole(w.kt < w.len / kKeys) {}
 };
 
 // Where the key of row r of a tile lies.  The page number is fetched a tile
@@ -770,8 +803,8 @@ __device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t ro
 // Loader warps fill the stages, tile by tile.  A half's barrier counts one
 // arrival a warp, and where rows come by asynchronous copies one a thread too.
 template <int FMT, int OP>
-__device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK,
-                                           bool& bad_page) {
+__device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* map, const Cursor& cur, Shared& sh,
+                                           uint32_t sQ, uint32_t sK, bool& bad_page) {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
   constexpr bool kDecode = R::kDecode;
@@ -779,16 +812,21 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, S
   const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - R::kLoad0), lane = static_cast<int>(threadIdx.x) & 31;
   const int row0 = R::kRows * warp;
   volatile uint32_t* ab = &sh.abort_flag;
-  // Lane i < kRows looks after row i of the warp's: its page number is fetched two tiles ahead.
+  // Lane i < kRows looks after row i of the warp's: its page number is fetched
+  // two tiles ahead.  Where tensor copies are made, lane kRows + i looks after
+  // box i of the tile: a tile that is all keys comes by one copy a box and slab.
   TileWalk w;  // two tiles ahead of the one being stored
   KeyAt at;
   Raw<kDecode ? FMT : MLA_CACHE_E4M3> raw;
-  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, row0 + lane, w.any && lane < R::kRows && !w.copied); };
+  const int boxes = !kDecode && p.box_rows > 0 ? kKeys / p.box_rows : 0;
+  const int look = lane < R::kRows ? row0 + lane : lane < R::kRows + boxes ? (lane - R::kRows) * p.box_rows : -1;
+  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
   w.start(cur);
   w.next(p, sh);
   Tile now(w);
   fetch();
   const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
+  int32_t mine_row = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);  // of a box
   w.next(p, sh);
   Tile then(w);
   fetch();
@@ -800,11 +838,40 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, S
     const bool first = uniform(now.first ? 1 : 0) != 0;
     const volatile SegmentInfo& info = sh.segments[now.seg & 7];
     const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * S::kImage;
+    bool boxed = false;  // the tile comes by tensor copies: every row is a key, every box has its page
+    if constexpr (!kDecode) {
+      if (boxes > 0 && direct) {
+        const bool mine_ok = mine != nullptr || lane < R::kRows || lane >= R::kRows + boxes;
+        boxed = now.whole && __all_sync(0xffffffffu, mine_ok) != 0;
+      }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t full = smem_u32(&sh.bars.kv_full[st][h]);
       if (round > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st][h]), (round - 1) & 1u, ab)) return false;
-      if (direct) {
+      if (boxed) {
+        constexpr uint32_t kHalf = S::kHalfSlabs * kSlabBytes;
+        if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = 1;
+        __syncwarp();
+        if (warp == 0) {
+          if (lane == R::kRows) {
+            arrive(full, kArrive - 1);
+            arrive_expect(full, kHalf + (h == 0 ? kSlabBytes : 0));
+          }
+          __syncwarp();
+          if (lane >= R::kRows && lane < R::kRows + boxes) {
+            const uint32_t dst = base + static_cast<uint32_t>(look) * 128u;
+            constexpr int kX = 128 / S::kElem;
+#pragma unroll
+            for (int s = 0; s < S::kHalfSlabs; ++s)
+              tensor_copy(dst + (h * S::kHalfSlabs + s) * kSlabBytes, map, (h * S::kHalfSlabs + s) * kX, mine_row, full);
+            if (h == 0) tensor_copy(dst + S::kPeSlab * kSlabBytes, map, S::kPeSlab * kX, mine_row, full);
+          }
+          __syncwarp();
+        } else {
+          if (lane == 0) arrive(full, kArrive);
+        }
+      } else if (direct) {
         if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = mine != nullptr ? 1 : 0;
         if constexpr (kDecode) {
           store_half<FMT>(raw, h, row0, lane,
@@ -841,6 +908,7 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, S
     }
     // the next tile's loads go out behind the fences, which would wait for them
     mine = at.address(p, row_bytes(FMT), bad_page);
+    mine_row = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
     if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
     now = then;
     w.next(p, sh);
@@ -855,9 +923,10 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Cursor& cur, S
 }
 
 template <int FMT, int OP>
-__device__ __forceinline__ void loader(const Params& p, const Cursor& cur, Shared& sh, uint32_t sQ, uint32_t sK) {
+__device__ __forceinline__ void loader(const Params& p, const CUtensorMap* map, const Cursor& cur, Shared& sh,
+                                       uint32_t sQ, uint32_t sK) {
   bool bad_page = false;
-  const bool good = load_tiles<FMT, OP>(p, cur, sh, sQ, sK, bad_page);
+  const bool good = load_tiles<FMT, OP>(p, map, cur, sh, sQ, sK, bad_page);
   // no copy may be under way when the CTA ends: on the way out after a timeout
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -949,12 +1018,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
     }
     if (left == 0 && v == s) break;
     const uint32_t s_buf = s & 1u;
-    const uint32_t got = __reduce_or_sync(
-        0xffffffffu, ask(smem_u32(&sh.bars.p_full), v & 1u, 0) | ask(smem_u32(&sh.bars.o_empty), (v_seg - 1) & 1u, 1) |
-                         ask(smem_u32(&sh.bars.kv_full[s_st][0]), s_round & 1u, 2) |
-                         ask(smem_u32(&sh.bars.kv_full[s_st][1]), s_round & 1u, 3) |
-                         ask(smem_u32(&sh.bars.q_full), (seg - 1) & 1u, 4) |
-                         ask(smem_u32(&sh.bars.s_empty[s_buf]), (s / 2 - 1) & 1u, 5));
+    const uint32_t bars[6] = {smem_u32(&sh.bars.p_full),           smem_u32(&sh.bars.o_empty),
+                              smem_u32(&sh.bars.kv_full[s_st][0]), smem_u32(&sh.bars.kv_full[s_st][1]),
+                              smem_u32(&sh.bars.q_full),           smem_u32(&sh.bars.s_empty[s_buf])};
+    const uint32_t parities[6] = {v & 1u,       (v_seg - 1) & 1u, s_round & 1u,
+                                  s_round & 1u, (seg - 1) & 1u,   (s / 2 - 1) & 1u};
+    const uint32_t got = ask(bars, parities);
     const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
     if (v < s && (got & 1u) != 0u && (!opens || v_seg == 0 || (got & 2u) != 0u)) {
       fence_after();
@@ -1039,12 +1108,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     float l = 0.0f;       // this thread's share of the denominator
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
       const uint32_t buf = it & 1u;
-      good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab) && good;
-      // complete by now; the flags may have come through it by the copy engine
+      // the flags first: they are there before the scores, and may have come by the copy engine
       good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab) && good;
-      fence_after();
-      uint32_t v[kN];
-      tmem_ld<kN>(tmem + kTmemS + 32u * buf + lanes + static_cast<uint32_t>(sub * kN), v);
       uint32_t ok[kN / 4];
 #pragma unroll
       for (int j = 0; j < kN / 16; ++j) {
@@ -1054,6 +1119,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
         ok[4 * j + 2] = f.z;
         ok[4 * j + 3] = f.w;
       }
+      uint32_t all = ok[0];
+#pragma unroll
+      for (int j = 1; j < kN / 4; ++j) all &= ok[j];
+      const bool whole = all == 0x01010101u;
+      good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab) && good;
+      fence_after();
+      uint32_t v[kN];
+      tmem_ld<kN>(tmem + kTmemS + 32u * buf + lanes + static_cast<uint32_t>(sub * kN), v);
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[buf]));
@@ -1065,10 +1138,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
 #pragma unroll
         for (int j = 0; j < kN; ++j) v[j] ^= 0x80000000u;
       }
-      uint32_t all = ok[0];
-#pragma unroll
-      for (int j = 1; j < kN / 4; ++j) all &= ok[j];
-      const bool whole = all == 0x01010101u;
       if (!whole) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) v[j] = (ok[j >> 2] >> (8 * (j & 3))) & 1u ? v[j] : 0xff800000u;
@@ -1270,7 +1339,8 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
 }
 
 template <int FMT, int OP>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap map, const Params p) {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
   // a half of a tile: one arrival a loader warp, and one a thread where rows come by asynchronous copies
@@ -1329,7 +1399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Params p) {
     } else if (warp == R::kMma) {
       mma_role<OP>(p, cur, sh, sQ, sK, sP, tmem);
     } else {
-      loader<FMT, OP>(p, cur, sh, sQ, sK);
+      loader<FMT, OP>(p, &map, cur, sh, sQ, sK);
     }
   }
   fence_before();
@@ -1554,10 +1624,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
 
 // ---- host ------------------------------------------------------------------------------
 
-// A prefix is decoded once, into the workspace, when its group has at least
-// kImageRows rows on average and the images fit kImageLimit; else its tiles
-// are read from the cache.
+// A prefix is decoded once, into the workspace, when its rows need decoding (or
+// pages are too small for tensor copies), its group has at least kImageRows rows
+// on average and the images fit kImageLimit; else its tiles are read from the
+// cache.
 constexpr int64_t kImageRows = 4 * kRowsTile;
+constexpr int kLeastBox = 8;  // rows of a tensor copy at least: the swizzle's period
 constexpr int64_t kImageLimit = INT64_C(1) << 31;
 
 struct Layout {
@@ -1601,6 +1673,31 @@ const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kerne
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 std::atomic<bool> g_smem_ready[kMaxDevices][4];
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+  if (fn == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+      known.store(fn, std::memory_order_release);
+    } else {
+      (void)cudaGetLastError();
+    }
+  }
+  return fn;
+}
+
+// The largest power of two up to 64 that divides a block's rows, so that a box
+// of that many rows, at a multiple of it in the sequence, lies in one page.
+int box_rows_of(int64_t block_size) {
+  int r = kKeys;
+  while (block_size % r != 0) r /= 2;
+  return r >= kLeastBox ? r : 0;
+}
 
 bool sizes_ok(int64_t T, int64_t H, int64_t G) {
   return T >= 0 && H >= 1 && H <= 65535 && T <= (static_cast<int64_t>(INT_MAX) - kRowsTile) / H && G >= 0 && G <= T;
@@ -1729,7 +1826,30 @@ mla_status mla_prefix_attend_launch(
     if (e != cudaSuccess) return mla::cuda_failure(e);
     g_smem_ready[dev][k].store(true, std::memory_order_release);
   }
+  // Tensor copies: rows of 16-bit values or codes as they are, in pages of a multiple of eight rows
+  CUtensorMap map{};
+  p.box_rows = 0;
+  const bool decode = k == MLA_CACHE_MX || k == MLA_CACHE_E4M3;
+  const int64_t cache_rows = num_blocks * block_size;
+  const int box = box_rows_of(block_size);
+  if (!decode && box > 0 && cache_rows > 0 && cache_rows < INT_MAX) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return mla::cuda_failure(cudaErrorNotSupported);
+    const cuuint64_t elem = k == 3 ? 1 : 2;
+    const cuuint64_t dims[2] = {576, static_cast<cuuint64_t>(cache_rows)};
+    const cuuint64_t strides[1] = {576 * elem};
+    const cuuint32_t size[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box)};
+    const cuuint32_t step[2] = {1, 1};
+    if (encode(&map, k == 3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+               const_cast<void*>(cache), dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MLA_ERR_INVALID_ARG;
+    p.box_rows = box;
+    p.image = nullptr;
+  }
   void* args[] = {&p};
+  void* attend_args[] = {&map, &p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;
   if (p.image != nullptr) {
     s = launch(ks.image, dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
@@ -1737,7 +1857,7 @@ mla_status mla_prefix_attend_launch(
     if (s != MLA_OK) return s;
     pdl = true;
   }
-  s = launch(ks.attend, dim3(static_cast<unsigned>(sms), 1, 1), kThreads, ks.smem, pdl, stream, args);
+  s = launch(ks.attend, dim3(static_cast<unsigned>(sms), 1, 1), kThreads, ks.smem, pdl, stream, attend_args);
   if (s != MLA_OK) return s;
 
   // slices: enough blocks for every SM to have some, a thread not below one chunk of columns
