@@ -77,11 +77,12 @@ struct Shape {
   static constexpr int kKeySteps = OP == kF8 ? 2 : 4;       // MMAs over a tile's keys, 32 or 16 keys each
   static constexpr uint32_t kTile = (kPeSlab + 1) * kSlabBytes;          // 72 or 40 KB
   static constexpr uint32_t kP = OP == kF8 ? 2 * kSlabBytes : kSlabBytes;
-  static constexpr int kStages = OP == kF8 ? 4 : 2;
-  static constexpr uint32_t kSmem = kTile * (1 + kStages) + kP + 1024;
+  static constexpr int kPBufs = OP == kF8 ? 2 : 1;          // (bf16 has no room for a second)
+  static constexpr int kStages = OP == kF8 ? 3 : 2;
+  static constexpr uint32_t kSmem = kTile * (1 + kStages) + kP * kPBufs + 1024;
   static constexpr uint32_t kImage = kTile + 128;           // a decoded tile as it lies in shared memory, then its 64 flags
 };
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
 
 // Roles.  Rows that need no decoding come by asynchronous copies, which four
 // warps issue easily, and leave eight warps for the softmax; decoding rows
@@ -548,7 +549,7 @@ struct Bars {
   uint64_t kv_full[kMaxStages][2], kv_empty[kMaxStages][2];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full, pv_done, o_empty;
+  uint64_t p_full[2], pv_done[2], o_empty;  // [tile & 1]
   uint64_t drained;
 };
 
@@ -702,6 +703,7 @@ struct TileWalk {
   __device__ __forceinline__ void start(const Cursor& c) {
     cur = c;
     kt = k1 = seg = len = 0;
+    table = nullptr;
     copied = first = false;
     any = true;
   }
@@ -820,9 +822,9 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
   Raw<kDecode ? FMT : MLA_CACHE_E4M3> raw;
   const int boxes = !kDecode && p.box_rows > 0 ? kKeys / p.box_rows : 0;
   const int look = lane < R::kRows ? row0 + lane : lane < R::kRows + boxes ? (lane - R::kRows) * p.box_rows : -1;
-  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
   w.start(cur);
   w.next(p, sh);
+  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
   Tile now(w);
   fetch();
   const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
@@ -850,27 +852,25 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
       const uint32_t full = smem_u32(&sh.bars.kv_full[st][h]);
       if (round > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st][h]), (round - 1) & 1u, ab)) return false;
       if (boxed) {
-        constexpr uint32_t kHalf = S::kHalfSlabs * kSlabBytes;
         if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = 1;
         __syncwarp();
-        if (warp == 0) {
-          if (lane == R::kRows) {
-            arrive(full, kArrive - 1);
-            arrive_expect(full, kHalf + (h == 0 ? kSlabBytes : 0));
-          }
-          __syncwarp();
-          if (lane >= R::kRows && lane < R::kRows + boxes) {
-            const uint32_t dst = base + static_cast<uint32_t>(look) * 128u;
-            constexpr int kX = 128 / S::kElem;
-#pragma unroll
-            for (int s = 0; s < S::kHalfSlabs; ++s)
-              tensor_copy(dst + (h * S::kHalfSlabs + s) * kSlabBytes, map, (h * S::kHalfSlabs + s) * kX, mine_row, full);
-            if (h == 0) tensor_copy(dst + S::kPeSlab * kSlabBytes, map, S::kPeSlab * kX, mine_row, full);
-          }
-          __syncwarp();
-        } else {
-          if (lane == 0) arrive(full, kArrive);
+        // the half's slabs over the loader warps: issuing one copy takes about 90 cycles
+        constexpr int kSlabs = S::kHalfSlabs;
+        const int extra = h == 0 && warp == kSlabs % R::kLoad ? 1 : 0;  // this warp copies the rotary slab
+        const int mine_slabs = (warp < kSlabs ? 1 : 0) + extra;
+        if (lane == R::kRows) {
+          arrive(full, kArrive - 1);
+          arrive_expect(full, static_cast<uint32_t>(mine_slabs) * kSlabBytes);
         }
+        __syncwarp();
+        if (lane >= R::kRows && lane < R::kRows + boxes) {
+          const uint32_t dst = base + static_cast<uint32_t>(look) * 128u;
+          constexpr int kX = 128 / S::kElem;
+          const int s = h * kSlabs + warp;
+          if (warp < kSlabs) tensor_copy(dst + static_cast<uint32_t>(s) * kSlabBytes, map, s * kX, mine_row, full);
+          if (extra != 0) tensor_copy(dst + S::kPeSlab * kSlabBytes, map, S::kPeSlab * kX, mine_row, full);
+        }
+        __syncwarp();
       } else if (direct) {
         if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = mine != nullptr ? 1 : 0;
         if constexpr (kDecode) {
@@ -966,12 +966,13 @@ __device__ __forceinline__ void pv_half(uint64_t p, uint64_t v, uint32_t tmem, i
 }
 
 template <int OP, bool FIRST>
-__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st) {
+__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st,
+                                            uint32_t buf) {
   pv_half<OP, FIRST>(p, v, tmem, 0);
   commit(smem_u32(&sh.bars.kv_empty[st][0]));
   pv_half<OP, FIRST>(p, v, tmem, 1);
   commit(smem_u32(&sh.bars.kv_empty[st][1]));
-  commit(smem_u32(&sh.bars.pv_done));
+  commit(smem_u32(&sh.bars.pv_done[buf]));
 }
 
 // Scores: MMAs over STEPS 32-byte pieces of the rows from slab S0 on.
@@ -1018,21 +1019,22 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
     }
     if (left == 0 && v == s) break;
     const uint32_t s_buf = s & 1u;
-    const uint32_t bars[6] = {smem_u32(&sh.bars.p_full),           smem_u32(&sh.bars.o_empty),
+    const uint32_t bars[6] = {smem_u32(&sh.bars.p_full[v & 1u]),   smem_u32(&sh.bars.o_empty),
                               smem_u32(&sh.bars.kv_full[s_st][0]), smem_u32(&sh.bars.kv_full[s_st][1]),
                               smem_u32(&sh.bars.q_full),           smem_u32(&sh.bars.s_empty[s_buf])};
-    const uint32_t parities[6] = {v & 1u,       (v_seg - 1) & 1u, s_round & 1u,
+    const uint32_t parities[6] = {(v / 2) & 1u, (v_seg - 1) & 1u, s_round & 1u,
                                   s_round & 1u, (seg - 1) & 1u,   (s / 2 - 1) & 1u};
     const uint32_t got = ask(bars, parities);
     const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
     if (v < s && (got & 1u) != 0u && (!opens || v_seg == 0 || (got & 2u) != 0u)) {
       fence_after();
       const uint64_t vd = dV + v_st * (S::kTile >> 4);
+      const uint64_t pd = dP + (S::kPBufs > 1 ? (v & 1u) * (S::kP >> 4) : 0u);
       if (opens) {
-        pv_products<OP, true>(sh, dP, vd, tmem, v_st);
+        pv_products<OP, true>(sh, pd, vd, tmem, v_st, v & 1u);
         ++v_seg;
       } else {
-        pv_products<OP, false>(sh, dP, vd, tmem, v_st);
+        pv_products<OP, false>(sh, pd, vd, tmem, v_st, v & 1u);
       }
       ++v;
       v_st = v_st + 1 == S::kStages ? 0 : v_st + 1;
@@ -1204,9 +1206,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
         }
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (it > 0)  // the previous tile's weights have been read, its products are in the sums
-        good = warp_wait(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
-      if (good && moved && !first) {
+      // the weights that were in this buffer have been read
+      constexpr uint32_t kBack = Shape<OP>::kPBufs;
+      if (it >= kBack) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - kBack) & 1u]), ((it - kBack) / 2) & 1u, ab);
+      if (moved && !first) {
+        // the previous tile's products are in the sums (all threads move or none)
+        if (kBack > 1) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab) && good;
         fence_after();
 #pragma unroll 1
         for (uint32_t c = 0; c < 1024u / WARPS; c += 32) {
@@ -1219,34 +1224,35 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
+      const uint32_t dst = sP + (kBack > 1 ? buf * Shape<OP>::kP : 0u);
       if constexpr (OP == kF8) {
 #pragma unroll
         for (int j = 0; j < kN / 16; ++j) {
           const int c = part * (kN / 16) + j;
-          st_shared(piece_addr(sP, 0, r, c), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
-          st_shared(piece_addr(sP, 0, r, 4 + c), make_uint4(mid[4 * j], mid[4 * j + 1], mid[4 * j + 2], mid[4 * j + 3]));
-          st_shared(piece_addr(sP, 1, r, c), make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]));
+          st_shared(piece_addr(dst, 0, r, c), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+          st_shared(piece_addr(dst, 0, r, 4 + c), make_uint4(mid[4 * j], mid[4 * j + 1], mid[4 * j + 2], mid[4 * j + 3]));
+          st_shared(piece_addr(dst, 1, r, c), make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]));
         }
       } else {
 #pragma unroll
         for (int j = 0; j < kN / 8; ++j)
-          st_shared(piece_addr(sP, 0, r, part * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+          st_shared(piece_addr(dst, 0, r, part * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
       }
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) arrive(smem_u32(&sh.bars.p_full));
+      if (lane == 0) arrive(smem_u32(&sh.bars.p_full[buf]));
     }
     if (!good) break;
     // ---- the segment's result
-    good = warp_wait(smem_u32(&sh.bars.pv_done), (it - 1) & 1u, ab);
+    good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab);
     if (bar_or(1, 32 * WARPS, !good)) {
       good = false;
       break;
     }
     fence_after();
     const bool keep = r < seg.rows;
-    uint4* dst = reinterpret_cast<uint4*>(seg.part) + r;
+    uint4* out = reinterpret_cast<uint4*>(seg.part) + r;
 #pragma unroll 1
     for (int i = 0; i < 1024 / WARPS; i += 32) {
       const int c = sub * 128 + i;
@@ -1257,7 +1263,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       if (keep) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          __stcg(dst + static_cast<int64_t>(chunk0 + j) * seg.part_rows,
+          __stcg(out + static_cast<int64_t>(chunk0 + j) * seg.part_rows,
                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
     }
@@ -1374,11 +1380,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       init(&sh.bars.s_full[i], 1);
       init(&sh.bars.s_empty[i], R::kSoft);
+      init(&sh.bars.p_full[i], R::kSoft);
+      init(&sh.bars.pv_done[i], 1);
     }
     init(&sh.bars.q_full, 32 * R::kLoad);
     init(&sh.bars.q_empty, 1);
-    init(&sh.bars.p_full, R::kSoft);
-    init(&sh.bars.pv_done, 1);
     init(&sh.bars.o_empty, R::kSoft);
     init(&sh.bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
