@@ -246,16 +246,18 @@ struct Segment {
 struct Cursor {
   int64_t pos, end;  // this CTA's run
   int64_t base, u;   // where unit u starts
+  const Unit* known;  // unit u, if it has been looked up already
 };
 
 __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment& s) {
   while (c.pos < c.end) {
     bool bad;
-    const Unit x = unit_at(p, c.u, bad);
+    const Unit x = c.known != nullptr ? *c.known : unit_at(p, c.u, bad);
     const int64_t per = x.row_cost(), n = x.row_tiles() * per;
     if (c.pos >= c.base + n) {
       c.base += n;
       ++c.u;
+      c.known = nullptr;
       continue;
     }
     const int64_t off = c.pos - c.base, r = off / per, from = off - r * per;
@@ -568,6 +570,7 @@ struct Shared {
   float xch[4][kRowsTile];
   int64_t warp_sum[kThreads / 32];
   int64_t first_unit, first_base;
+  Unit unit;  // the first unit: every role starts with it
 };
 
 // ---- the loaders' pieces --------------------------------------------------------
@@ -827,6 +830,11 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
   auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
   Tile now(w);
   fetch();
+  // the first segment's q rows go out while page numbers are under way
+  if (uniform(now.any ? 1 : 0) != 0) {
+    const volatile SegmentInfo& info = sh.segments[now.seg & 7];
+    load_q<FMT, OP>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
+  }
   const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
   int32_t mine_row = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);  // of a box
   w.next(p, sh);
@@ -900,9 +908,9 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
       } else {
         if (lane == 0) arrive(full, kArrive);
       }
-      if (h == 0 && first) {
+      if (h == 0 && first && now.seg > 1) {
         // the segment's q rows, once the previous segment's scores have been computed
-        if (now.seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
+        if (!warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
         load_q<FMT, OP>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
       }
     }
@@ -1298,9 +1306,11 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   int64_t sum = 0;
   bool any_bad = false;
+  Unit last{};  // the thread's last unit: its only one as a rule, and then not looked up again
   for (int64_t u = u0; u < u1; ++u) {
     bool bad;
-    sum += unit_at(p, u, bad).cost();
+    last = unit_at(p, u, bad);
+    sum += last.cost();
     any_bad = any_bad || bad;
   }
   if (any_bad && blockIdx.x == 0) report(p.status, MLA_STATUS_LEN_RANGE);
@@ -1329,18 +1339,20 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   if (mine || blockIdx.x == 0) {
     for (int64_t u = u0; u < u1; ++u) {
       bool bad;
-      const int64_t n = unit_at(p, u, bad).cost();
+      const Unit x = u + 1 == u1 ? last : unit_at(p, u, bad);
       if (blockIdx.x == 0) p.plan[1 + u] = base;
-      if (c.pos >= base && c.pos < base + n) {
+      if (c.pos >= base && c.pos < base + x.cost()) {
         sh.first_unit = u;
         sh.first_base = base;
+        sh.unit = x;
       }
-      base += n;
+      base += x.cost();
     }
   }
   __syncthreads();
   c.u = sh.first_unit;
   c.base = sh.first_base;
+  c.known = &sh.unit;
   return c;
 }
 
@@ -1389,6 +1401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(&sh.bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 32 && p.box_rows > 0)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
   pdl_wait();     // the lengths, q and the cache rows may come from the upstream kernel
   pdl_trigger();  // the joining kernel waits for this grid's end itself
   fence_before();
@@ -1462,16 +1476,17 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
 // ---- joining a row's segments ----------------------------------------------------------
 //
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A block takes one token,
-// 16 of its heads and a slice of the columns; thread (row, worker).  A thread's
-// first sums are loaded before the weights they need are known, so the chain is
-// plan, statistics and sums: few trips to memory, whatever n is.  With few
-// tokens the columns are cut into more slices and a row's segments shared out
-// to classes of workers.
+// 16 of its heads and a slice of the columns; thread (row, worker), CH chunks of
+// four columns at a time.  A thread's first sums are loaded before the weights
+// they need are known, so the chain is plan, statistics and sums: few trips to
+// memory, whatever n is.  With few tokens the columns are cut into more slices
+// and a row's segments shared out to classes of workers.
 
 constexpr int kJoinRows = 16, kJoinWorkers = 16, kJoinThreads = kJoinRows * kJoinWorkers;
-constexpr int kJoinAhead = 6;
 
+template <int CH>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int slices) {
+  constexpr int kAhead = 8 / CH;      // segments loaded ahead
   extern __shared__ float weights[];  // [segments][16]
   __shared__ float red[2][kJoinWorkers][kJoinRows];
   __shared__ float4 sums[kJoinWorkers][kJoinRows];
@@ -1487,9 +1502,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
 
   // the row's segments: n1 of its group's prefix, n2 of its own keys
   const int64_t each = __ldcg(p.plan);
-  int64_t at1 = 0, at2 = 0;
-  int n1 = 0, n2 = 0, prow = 0;
-  const int orow = h % kRowsTile;
+  int n1 = 0, n2 = 0;
+  const uint8_t* part1 = p.prefix_part;  // its first segment of either kind, and the row in it
+  const uint8_t* part2 = p.own_part;
+  int row1 = 0;
+  const int row2 = h % kRowsTile;
   if (live) {
     int64_t g = -1;
     if (p.G > 0 && p.group_offsets == nullptr) {
@@ -1503,62 +1520,65 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
       g = lo - 1;
     }
     // CTAs c0 .. c1 have the row's key tiles
-    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int64_t& at, int& n) {
+    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int rows, const uint8_t*& part, int& n) {
       const int64_t per = x.row_cost();
       if (per == 0) return;
       const int64_t f = __ldcg(p.plan + 1 + unit) + tile * per;
       const int64_t c0 = (f + kCostSegment) / each, c1 = (f + per - x.tile_cost) / each;
-      at = c0 + x.part0 + tile;
+      part += (c0 + x.part0 + tile) * part_bytes(rows);
       n = static_cast<int>(c1 - c0) + 1;
     };
     bool bad;
     const Unit own = unit_at(p, p.G + t, bad);
-    span(own, p.G + t, h / kRowsTile, at2, n2);
+    span(own, p.G + t, h / kRowsTile, p.own_rows, part2, n2);
     if (g >= 0) {
       const Unit x = unit_at(p, g, bad);
       const int64_t i = t * p.H + h - x.rows0;
       if (i >= 0 && i < x.rows) {
-        span(x, g, i / kRowsTile, at1, n1);
-        prow = static_cast<int>(i % kRowsTile);
+        span(x, g, i / kRowsTile, kRowsTile, part1, n1);
+        row1 = static_cast<int>(i % kRowsTile);
       }
     }
   }
   const int n = n1 + n2;
-  // segment i: its sums, and its statistics
-  auto sums_of = [&](int i, int chunk) -> float4 {
+  // segment i, its rows and the row in it
+  auto part_of = [&](int i, int& rows, int& r) -> const uint8_t* {
     const bool pre = i < n1;
-    const uint8_t* part = pre ? p.prefix_part + (at1 + i) * part_bytes(kRowsTile)
-                              : p.own_part + (at2 + i - n1) * part_bytes(p.own_rows);
-    return __ldcg(reinterpret_cast<const float4*>(part) + static_cast<int64_t>(chunk) * (pre ? kRowsTile : p.own_rows) +
-                  (pre ? prow : orow));
+    rows = pre ? kRowsTile : p.own_rows;
+    r = pre ? row1 : row2;
+    return pre ? part1 + i * part_bytes(kRowsTile) : part2 + (i - n1) * part_bytes(p.own_rows);
   };
   auto stats_of = [&](int i, float& m, float& l) {
-    const bool pre = i < n1;
-    const int rows = pre ? kRowsTile : p.own_rows;
-    const uint8_t* part = pre ? p.prefix_part + (at1 + i) * part_bytes(kRowsTile)
-                              : p.own_part + (at2 + i - n1) * part_bytes(p.own_rows);
-    const float* s = reinterpret_cast<const float*>(part + static_cast<int64_t>(rows) * kChunks * 16) + (pre ? prow : orow);
+    int rows, r;
+    const uint8_t* part = part_of(i, rows, r);
+    const float* s = reinterpret_cast<const float*>(part + static_cast<int64_t>(rows) * kChunks * 16) + r;
     m = __ldcg(s);
     l = __ldcg(s + rows);
   };
 
-  // `per` chunks of 4 columns in this slice, cw of them at a time, 16 / cw segment classes
+  // `per` chunks in this slice; workers: cw columns of chunks, 16 / cw segment classes
   const int per = kChunks / slices;
-  const int cw = per < kJoinWorkers ? per : kJoinWorkers;
+  const int cw = per / CH < kJoinWorkers ? per / CH : kJoinWorkers;
   const int classes = kJoinWorkers / cw;
   const int cls = wk / cw;
   const int chunk0 = slice * per + wk % cw;
-  float4 ahead[kJoinAhead];
+  auto load = [&](int i, int c0, float4 (&o)[CH]) {
+    int rows, r;
+    const float4* part = reinterpret_cast<const float4*>(part_of(i, rows, r)) + r;
 #pragma unroll
-  for (int j = 0; j < kJoinAhead; ++j) {
+    for (int k = 0; k < CH; ++k) o[k] = __ldcg(part + (chunk0 + c0 + k * cw) * rows);
+  };
+  float4 ahead[kAhead][CH];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
     const int i = cls + j * classes;
-    ahead[j] = i < n ? sums_of(i, chunk0) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < n) load(i, 0, ahead[j]);
   }
 
   // ---- weights
-  float top = -INFINITY, m0 = -INFINITY, l0 = 0.0f;
+  float m0 = -INFINITY, l0 = 0.0f;
   if (wk < n) stats_of(wk, m0, l0);
-  top = m0;
+  float top = m0;
   for (int i = wk + kJoinWorkers; i < n; i += kJoinWorkers) {
     float m, l;
     stats_of(i, m, l);
@@ -1588,41 +1608,56 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   if (p.kv_scale != nullptr) mul *= __ldcg(p.kv_scale);
 
   // ---- sums
-  for (int c0 = 0; c0 < per; c0 += cw) {
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto add = [&](int i, const float4& o) {
+  for (int c0 = 0; c0 < per; c0 += cw * CH) {
+    float4 acc[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](int i, const float4 (&o)[CH]) {
       const float w = weights[i * kJoinRows + row];
-      acc.x += w * o.x;
-      acc.y += w * o.y;
-      acc.z += w * o.z;
-      acc.w += w * o.w;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        acc[k].x += w * o[k].x;
+        acc[k].y += w * o[k].y;
+        acc[k].z += w * o[k].z;
+        acc[k].w += w * o[k].w;
+      }
     };
     int i = cls;
     if (c0 == 0) {
 #pragma unroll
-      for (int j = 0; j < kJoinAhead; ++j, i += classes)
+      for (int j = 0; j < kAhead; ++j, i += classes)
         if (i < n) add(i, ahead[j]);
     }
-#pragma unroll 4
-    for (; i < n; i += classes) add(i, sums_of(i, chunk0 + c0));
-    if (classes > 1) {
+    for (; i < n; i += 4 * classes) {
+      float4 o[4][CH];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j * classes < n) load(i + j * classes, c0, o[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j * classes < n) add(i + j * classes, o[j]);
+    }
+    if (CH == 1 && classes > 1) {
       __syncthreads();
-      sums[wk][row] = acc;
+      sums[wk][row] = acc[0];
       __syncthreads();
       if (cls == 0) {
         for (int k = 1; k < classes; ++k) {
           const float4 o = sums[k * cw + wk % cw][row];
-          acc.x += o.x;
-          acc.y += o.y;
-          acc.z += o.z;
-          acc.w += o.w;
+          acc[0].x += o.x;
+          acc[0].y += o.y;
+          acc[0].z += o.z;
+          acc[0].w += o.w;
         }
       }
     }
     if (live && cls == 0) {
-      uint2 o = make_uint2(pack_bf16x2(acc.x * mul, acc.y * mul), pack_bf16x2(acc.z * mul, acc.w * mul));
-      if (n == 0) o = make_uint2(0, 0);
-      *reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kDv + 4 * (chunk0 + c0)) = o;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        uint2 o = make_uint2(pack_bf16x2(acc[k].x * mul, acc[k].y * mul), pack_bf16x2(acc[k].z * mul, acc[k].w * mul));
+        if (n == 0) o = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kDv + 4 * (chunk0 + c0 + k * cw)) = o;
+      }
     }
   }
   pdl_trigger();
@@ -1871,8 +1906,11 @@ mla_status mla_prefix_attend_launch(
   int32_t slices = 1;
   while (slices < 32 && rows * slices < 2 * sms) slices *= 2;
   void* jargs[] = {&p, &slices};
-  return launch(reinterpret_cast<const void*>(&join_kernel), dim3(static_cast<unsigned>(rows * slices), 1, 1),
-                kJoinThreads, static_cast<size_t>(2 * sms) * kJoinRows * sizeof(float), true, stream, jargs);
+  const void* join = slices <= 2   ? reinterpret_cast<const void*>(&join_kernel<4>)
+                     : slices == 4 ? reinterpret_cast<const void*>(&join_kernel<2>)
+                                   : reinterpret_cast<const void*>(&join_kernel<1>);
+  return launch(join, dim3(static_cast<unsigned>(rows * slices), 1, 1), kJoinThreads,
+                static_cast<size_t>(2 * sms) * kJoinRows * sizeof(float), true, stream, jargs);
 }
 
 }  // extern "C"
