@@ -15,6 +15,7 @@ NOPE, PE, ROW, GROUP = 512, 64, 576, 32
 BF16, E4M3, MX = 0, 1, 2
 ROW_BYTES = {BF16: 1152, E4M3: 576, MX: 656}
 EPS_BF16, EPS_F16 = 2.0 ** -8, 2.0 ** -11  # half a step, relative
+EPS_F8_WEIGHT = 2.0 ** -9 + EPS_F16  # an fp16 weight as three e5m2 terms: each leaves half a step, 2^-3, of what it took
 
 
 def _lut():
@@ -109,7 +110,7 @@ def values(rows: np.ndarray, fmt: int, kv_scale=None) -> np.ndarray:
     return np.concatenate([x.reshape(-1, NOPE), pe], 1)
 
 
-def attend(q, keys, sm_scale, f16=False):
+def attend(q, keys, sm_scale, f8=False):
     """One token: q fp64 [H, 576], keys fp64 [n, 576].  Returns out [H, 512], lse [H] and the bounds of what the
     kernel's arithmetic may be off by.
 
@@ -117,8 +118,9 @@ def attend(q, keys, sm_scale, f16=False):
     order, truncating adders allowed), and the scale, the difference to the reference maximum and the power of two
     add a few units of 2^-23 of |s| and 2^-21.  A weight's relative error is that, d, plus half a step of its type,
     w; so the sum is off by (w + d) sum p |v| and the denominator by d, and the result by half a bf16 step.  The
-    fp32 sum of the products adds n * 2^-23 of sum p |v|.  A weight below the type's normal range (fp16) is off by
-    up to 2^-25 of the largest.
+    fp32 sum of the products adds n * 2^-23 of sum p |v|.  With e4m3 operands (f8) a weight is 2^7 times its power
+    of two as fp16 and then as three e5m2 terms; the last term's smallest step is 2^-16, so a small weight is off by
+    up to 2^-17 / 2^7 = 2^-24 of the reference weight, which is no larger than the row's largest.
     """
     H, n = q.shape[0], keys.shape[0]
     if n == 0:
@@ -134,10 +136,10 @@ def attend(q, keys, sm_scale, f16=False):
     out = p @ v
     lse = top[:, 0] + np.log(den[:, 0])
     d = (576 * 2.0 ** -23 * mag + 8 * 2.0 ** -23 * np.abs(s)).max(1, keepdims=True) + 2.0 ** -21
-    w = EPS_F16 if f16 else EPS_BF16
+    w = EPS_F8_WEIGHT if f8 else EPS_BF16
     pv = p @ np.abs(v)
     tol = (w + 2 * d + n * 2.0 ** -23) * pv + EPS_BF16 * np.abs(out) * 1.01 + 1e-30
-    if f16:
-        tol = tol + 2.0 ** -25 * 256 * np.abs(v).sum(0) / np.maximum(den, 1.0)
+    if f8:
+        tol = tol + 2.0 ** -24 * np.abs(v).sum(0) / den
     lse_tol = d[:, 0] + (n + 8) * 2.0 ** -23 + np.abs(lse) * 2.0 ** -21
     return out, lse, tol, lse_tol

@@ -303,9 +303,9 @@ class _Case:
 
     def check(self, out, lse):
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
-        f16 = self.fmt == R.E4M3 and self.q_scale is not None
+        f8 = self.fmt == R.E4M3 and self.q_scale is not None
         for t in range(len(self.lens)):
-            o, s, tol, stol = R.attend(self.q64[t], self.keys_of(t), self.sm_scale, f16)
+            o, s, tol, stol = R.attend(self.q64[t], self.keys_of(t), self.sm_scale, f8)
             bad = ~(np.abs(out[t] - o) <= tol)
             assert not bad.any(), (t, int(bad.sum()), np.abs(out[t] - o).max(), tol.max())
             if np.isinf(s).any():
@@ -526,6 +526,111 @@ def test_captured_step_replays_with_new_lengths():
             g2.replay()
     torch.cuda.synchronize()
     case.check(o1, l1), other.check(o2, l2)
+
+
+def test_attend_negative_scale():
+    case = _Case(R.BF16, 16, [130, 0, 70], prefixes=[100], seed=60)
+    case.sm_scale = -0.05
+    _run(case)
+    case = _Case(R.E4M3, 16, [130, 0, 70], prefixes=[100], q8=True, seed=61)
+    case.sm_scale = -0.05
+    _run(case)
+
+
+@pytest.mark.parametrize("fmt,q8", KINDS, ids=KIND_IDS)
+def test_attend_large_prefix_groups_of_many_rows(fmt, q8):
+    """Groups large enough for decoded tiles (where rows are decoded), over pages that are and are not whole boxes."""
+    lens = [(13 * i) % 50 for i in range(40)]
+    for block in (64, 20):
+        _run(_Case(fmt, 32, lens, prefixes=[300, 129], members=[0, 17, 40], block=block, q8=q8, seed=62 + block))
+
+
+def test_attend_missing_page_in_a_large_prefix():
+    for fmt, q8, block in ((R.MX, False, 64), (R.BF16, False, 64), (R.E4M3, True, 64), (R.BF16, False, 20)):
+        case = _Case(fmt, 32, [3] * 20, prefixes=[6 * block], block=block, q8=q8, seed=70)
+        case.prefix_table[0, 2] = -1
+        case.keys[0] = np.delete(case.keys[0], np.s_[2 * block:3 * block], axis=0)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = case.call(status=status)
+        case.check(out, lse)
+        assert int(status.item()) == E.MLA_STATUS_SLOT_RANGE
+
+
+@pytest.mark.parametrize("fmt,q8", KINDS, ids=KIND_IDS)
+def test_attend_values_at_the_ends_of_the_types(fmt, q8):
+    """NaN and infinite latents reach exactly the tokens that attend to them."""
+    case = _Case(fmt, 16, [70, 65, 5], q8=q8, seed=80)
+    raw = case.cache.view(torch.uint8).view(-1, R.ROW_BYTES[fmt])
+    page = int(case.table[1, 0])
+    slot = page * case.block + 3  # token 1, key 3: value 7 becomes NaN
+    if fmt == R.BF16:
+        raw[slot].view(torch.bfloat16)[7] = float("nan")
+    else:
+        raw[slot, 7] = 0x7F
+    out, lse = case.call()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    case.lens, out, lse = [70, 0, 5], out.clone(), lse.clone()
+    out[1], lse[1] = 0, float("-inf")
+    case.keys[1] = case.keys[1][:0]
+    case.check(out, lse)
+
+
+def test_attend_codes_of_every_value():
+    """All finite e4m3 codes and a wide range of scale exponents through the decoding."""
+    g = torch.Generator().manual_seed(90)
+    for fmt, q8 in ((R.E4M3, True), (R.E4M3, False), (R.MX, False)):
+        n, block = 256, 64
+        raw = _good_rows(g, n, fmt)
+        if fmt == R.MX:
+            raw[:, 512:528] = torch.randint(100, 140, (n, 16), generator=g).numpy()
+            raw[:, 512:514] = torch.randint(134, 136, (n, 2), generator=g).numpy()
+        val = R.values(raw, fmt, 1.0)
+        q = _bf(g, 1, 16, 576, std=0.01)
+        if q8:
+            qr = R.e4m3_bytes((q.float().numpy() / np.float32(SCALE)).astype(np.float64))
+            qd, qs, q64 = torch.from_numpy(qr).cuda(), torch.full((1,), SCALE, device="cuda"), R.LUT[qr] * float(np.float32(SCALE))
+        else:
+            qd, qs, q64 = q.cuda(), None, q.double().numpy()
+        scale = 2.0 ** -10
+        out, lse = L.mla_prefix_decode_attention(
+            qd, _cache(raw, fmt, block), torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda"),
+            sm_scale=scale, q_scale=qs, kv_scale=torch.ones(1, device="cuda") if fmt == R.E4M3 else None)
+        o, s, tol, stol = R.attend(q64[0], val, scale, q8)
+        assert (np.abs(out[0].double().cpu().numpy() - o) <= tol).all()
+        assert (np.abs(lse[0].double().cpu().numpy() - s) <= stol).all()
+
+
+def test_torch_forms_reject_wrong_tensors():
+    case = _Case(R.BF16, 4, [5, 6], prefixes=[20], seed=95)
+    good = dict(sm_scale=1.0, prefix_table=case.prefix_table, prefix_lens=case.prefix_lens)
+    call = L.mla_prefix_decode_attention
+    q, c, t, n = case.q, case.cache, case.table, case.seq_lens
+    for args, kw in (((q.float(), c, t, n), {}), ((q[..., :575], c, t, n), {}), ((q, c[..., :575], t, n), {}),
+                     ((q, c, t.long(), n), {}), ((q, c, t[:1], n), {}), ((q, c, t, n.long()), {}), ((q, c, t, None), {}),
+                     ((q, c, t.cpu(), n), {}), ((q, c, t, n), dict(kv_scale=torch.ones(1, device="cuda"))),
+                     ((q, c, t, n), dict(q_scale=torch.ones(1, device="cuda"))),
+                     ((q, c, t, n), dict(prefix_lens=None)), ((q, c, t, n), dict(prefix_table=None)),
+                     ((q, c, t, n), dict(group_offsets=torch.zeros(3, dtype=torch.int32, device="cuda"))),
+                     ((q, c, t, n), dict(out=torch.empty((2, 4, 512), device="cuda"))),
+                     ((q, c, t, n), dict(lse=torch.empty((2, 5), device="cuda"))),
+                     ((q, c, t, n), dict(status=torch.zeros(2, dtype=torch.int32, device="cuda")))):
+        with pytest.raises(ValueError):
+            call(*args, **{**good, **kw})
+    with pytest.raises(E.MlaError):  # too small a workspace
+        call(q, c, t, n, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"), **good)
+    x, pe = torch.zeros((3, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    for args, kw in (((x.float(), pe, c, slots), {}), ((x, pe[:2], c, slots), {}), ((x, pe, c, slots.int()), {}),
+                     ((x, pe, c, slots), dict(norm_weight=torch.ones(512, device="cuda"))),
+                     ((x, pe, c, slots), dict(positions=torch.zeros(3, dtype=torch.int32, device="cuda"))),
+                     ((x.t().contiguous().t(), pe, c, slots), {})):
+        with pytest.raises(ValueError):
+            L.mla_latent_cache_insert(*args, **kw)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for args, kw in (((c, t, cu[:2], 4), {}), ((c, t, cu.long(), 4), {}), ((c, t, cu, 4), dict(first=cu)),
+                     ((c, t, cu, 4), dict(out=torch.empty((5, 576), dtype=torch.bfloat16, device="cuda")))):
+        with pytest.raises(ValueError):
+            L.mla_latent_cache_gather(*args, **kw)
 
 
 def test_calls_on_two_streams_at_once():
