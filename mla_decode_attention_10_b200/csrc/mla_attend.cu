@@ -80,6 +80,7 @@ struct Shape {
   static constexpr int kPBufs = OP == kF8 ? 2 : 1;          // (bf16 has no room for a second)
   static constexpr int kStages = OP == kF8 ? 3 : 2;
   static constexpr uint32_t kSmem = kTile * (1 + kStages) + kP * kPBufs + 1024;
+  static constexpr uint32_t kImage = kTile + 128;           // a decoded tile as it lies in shared memory, then its 64 flags
 };
 constexpr int kMaxStages = 3;
 
@@ -104,10 +105,8 @@ constexpr float kRescale = 8.0f;       // the reference maximum moves when a sco
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
 // What the deal counts (measured cycles, in hundreds): a key tile, by how it
-// comes, a pair's step of two tiles, and a segment's start and end.
-constexpr int kCostRows = 34, kCostCodes = 60, kCostF8 = 25, kCostStep = 30, kCostSegment = 70;
-// A decoded tile of a prefix in the workspace, as it lies in shared memory, and its 64 flags.
-constexpr uint32_t kImage = Shape<kBf16>::kTile + 128;
+// comes, and a segment's start and end.
+constexpr int kCostImage = 30, kCostRows = 36, kCostCodes = 60, kCostF8 = 22, kCostSegment = 70;
 
 struct Params {
   const uint8_t* q;
@@ -129,15 +128,16 @@ struct Params {
   float sm_scale;
   uint16_t* out;
   float* lse;
-  int64_t* plan;      // [0] a CTA's run, [1] a pair's, [2 + u] where unit u starts
-  uint8_t* image;     // decoded prefix tiles: prefixes are the pairs'; or null: they are read from the cache
-  int64_t image_tiles;  // tiles of one group's image, an even number
+  int64_t* plan;      // [0] each CTA's run, [1 + u] where unit u starts
+  uint8_t* image;     // decoded prefix tiles, or null: prefixes are read from the cache
+  int64_t image_tiles;  // tiles of one group's image
   uint8_t* prefix_part;
   uint8_t* own_part;
   int32_t own_rows;   // rows of an own segment: min(H, 64)
   int32_t ctas;       // CTAs of the attention kernel
+  int32_t image_bytes;  // of one tile's image
   int32_t box_rows;     // cache rows of one tensor copy (8, 16, 32 or 64), or 0: none are made
-  int32_t tile_cost;    // of a tile read from the cache
+  int32_t tile_cost, image_cost;  // of a tile read from the cache, from an image
   int32_t* status;
 };
 
@@ -164,13 +164,13 @@ struct Unit {
   int64_t rows;
   int64_t len;    // keys
   const int32_t* table;
+  const uint8_t* image;  // its decoded tiles, or null
   bool prefix;
   int64_t part0;  // number of the first row tile, within the unit's kind
-  // The deal's grain: row tiles of `tile_rows` rows, key tiles (steps of a pair) of `tile_keys` keys.
-  int32_t tile_rows, tile_keys, tile_cost;
 
-  __device__ __forceinline__ int64_t row_tiles() const { return (rows + tile_rows - 1) / tile_rows; }
-  __device__ __forceinline__ int64_t key_tiles() const { return (len + tile_keys - 1) / tile_keys; }
+  __device__ __forceinline__ int64_t row_tiles() const { return (rows + kRowsTile - 1) / kRowsTile; }
+  __device__ __forceinline__ int64_t key_tiles() const { return (len + kKeys - 1) / kKeys; }
+  int32_t tile_cost;
   // what one row tile counts for in the deal: its start, then its key tiles
   __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() * tile_cost + kCostSegment : 0; }
   // the first key tile that starts at or behind position x of the row tile
@@ -197,9 +197,8 @@ __device__ __forceinline__ void group_tokens(const Params& p, int64_t g, int64_t
 }
 
 // Unit u: group u for u < G, else token u - G.  `bad`: something had to be cut.
-// Row tiles are numbered from rows0 / 64 + g on for a group (a pair's, two by
-// two, from 2 (rows0 / 128 + g) on): floor(x) + 1 >= ceil(x), so the numbers of
-// consecutive groups do not meet.
+// Row tiles are numbered from rows0 / 64 + g on for a group: floor(x) + 1 >=
+// ceil(x), so the numbers of consecutive groups do not meet.
 __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
   Unit x;
   int64_t len, keys;
@@ -211,12 +210,9 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
     x.rows0 = lo * p.H;
     x.rows = (hi - lo) * p.H;
     x.table = p.prefix_table + u * p.prefix_stride;
+    x.image = p.image != nullptr ? p.image + u * p.image_tiles * p.image_bytes : nullptr;
     x.prefix = true;
-    const bool paired = p.image != nullptr;
-    x.tile_rows = paired ? 2 * kRowsTile : kRowsTile;
-    x.tile_keys = paired ? 2 * kKeys : kKeys;
-    x.tile_cost = paired ? kCostStep : p.tile_cost;
-    x.part0 = (x.rows0 / x.tile_rows + u) * (paired ? 2 : 1);
+    x.part0 = x.rows0 / kRowsTile + u;
   } else {
     const int64_t t = u - p.G;
     bad = false;
@@ -225,25 +221,24 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
     x.rows0 = t * p.H;
     x.rows = p.H;
     x.table = p.block_table + t * p.table_stride;
+    x.image = nullptr;
     x.prefix = false;
-    x.tile_rows = kRowsTile;
-    x.tile_keys = kKeys;
-    x.tile_cost = p.tile_cost;
     x.part0 = t * ((p.H + kRowsTile - 1) / kRowsTile);
   }
   bad = bad || len > keys;
   x.len = cut(len, 0, keys);
+  x.tile_cost = x.image != nullptr ? p.image_cost : p.tile_cost;
   return x;
 }
 
-// One segment: rows [row0, row0 + rows) against key tiles [k0, k1) of unit u.
+// One segment: rows [row0, row0 + rows) against key tiles [k0, k1).
 struct Segment {
-  int64_t u;
   int64_t row0;
   int32_t rows;
   int32_t k0, k1;
   int64_t len;
   const int32_t* table;
+  const uint8_t* image;
   uint8_t* part;
   int32_t part_rows;
 };
@@ -254,9 +249,7 @@ struct Cursor {
   const Unit* known;  // unit u, if it has been looked up already
 };
 
-// The next segment of a CTA's run, or (PAIR) of a pair's run the part of its CTA `rank`.
-template <bool PAIR = false>
-__device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment& s, int rank = 0) {
+__device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment& s) {
   while (c.pos < c.end) {
     bool bad;
     const Unit x = c.known != nullptr ? *c.known : unit_at(p, c.u, bad);
@@ -273,19 +266,17 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
     // the key tiles that start in this run
     const int64_t k = x.tile_at(from), k_end = to < per ? x.tile_at(to) : x.key_tiles();
     if (k >= k_end) continue;
-    const int64_t skip = r * x.tile_rows + rank * kRowsTile, rows = cut(x.rows - skip, 0, kRowsTile);
-    s.u = c.u;
-    s.row0 = x.rows0 + skip;
-    s.rows = static_cast<int32_t>(rows);
+    s.row0 = x.rows0 + r * kRowsTile;
+    s.rows = static_cast<int32_t>(x.rows - r * kRowsTile < kRowsTile ? x.rows - r * kRowsTile : kRowsTile);
     s.k0 = static_cast<int32_t>(k);
     s.k1 = static_cast<int32_t>(k_end);
     s.len = x.len;
     s.table = x.table;
+    s.image = x.image;
     s.part_rows = x.prefix ? kRowsTile : p.own_rows;
-    // Segments ascend in (CTA, row tile), so CTA + row tile numbers each one
-    // (a pair's two parts: 2 pair + 2 row tile + rank).
-    const int64_t at = PAIR ? 2 * (static_cast<int64_t>(blockIdx.x) / 2 + r) + rank : blockIdx.x + r;
-    s.part = (x.prefix ? p.prefix_part : p.own_part) + (at + x.part0) * part_bytes(s.part_rows);
+    // segments ascend in (CTA, row tile), so CTA + row tile numbers each one
+    s.part = (x.prefix ? p.prefix_part : p.own_part) +
+             (static_cast<int64_t>(blockIdx.x) + x.part0 + r) * part_bytes(s.part_rows);
     return true;
   }
   return false;
@@ -565,6 +556,7 @@ struct Bars {
 };
 
 struct SegmentInfo {
+  const uint8_t* image;
   int32_t row0, rows;  // q rows
 };
 
@@ -707,6 +699,7 @@ struct TileWalk {
   const int32_t* table;
   int32_t len, kt, k1;
   int32_t seg;   // segments begun
+  bool copied;   // the segment's tiles come from an image
   bool first;    // the tile is its segment's first
   bool any;      // not yet behind the last
 
@@ -714,7 +707,7 @@ struct TileWalk {
     cur = c;
     kt = k1 = seg = len = 0;
     table = nullptr;
-    first = false;
+    copied = first = false;
     any = true;
   }
   // To the next tile.
@@ -729,10 +722,12 @@ struct TileWalk {
     len = static_cast<int32_t>(s.len);
     kt = s.k0;
     k1 = s.k1;
+    copied = s.image != nullptr;
     ++seg;
     // Kept for the tiles' own turn.  Every loader warp writes the same values;
     // they are at most 2 + 2 + 1 segments apart, so none is overwritten too early.
     volatile SegmentInfo& i = sh.segments[seg & 7];
+    i.image = s.image;
     i.row0 = static_cast<int32_t>(s.row0);
     i.rows = s.rows;
   }
@@ -740,10 +735,10 @@ struct TileWalk {
 
 struct Tile {
   int32_t kt, seg;
-  bool first, any, whole;  // whole: no key behind the sequence's end
+  bool copied, first, any, whole;  // whole: no key behind the sequence's end
 
   __device__ __forceinline__ explicit Tile(const TileWalk& w)
-      : kt(w.kt), seg(w.seg), first(w.first), any(w.any), whole(w.kt < w.len / kKeys) {}
+      : kt(w.kt), seg(w.seg), copied(w.copied), first(w.first), any(w.any), whole(w.kt < w.len / kKeys) {}
 };
 
 // Where the key of row r of a tile lies.  The page number is fetched a tile
@@ -832,7 +827,7 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
   const int look = lane < R::kRows ? row0 + lane : lane < R::kRows + boxes ? (lane - R::kRows) * p.box_rows : -1;
   w.start(cur);
   w.next(p, sh);
-  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0); };
+  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
   Tile now(w);
   fetch();
   // the first segment's q rows go out while page numbers are under way
@@ -849,11 +844,13 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
   uint32_t st = 0, round = 0;  // stage, and how often the stages have been round
   while (uniform(now.any ? 1 : 0) != 0) {
     const uint32_t base = sK + st * S::kTile;
+    const bool direct = uniform(now.copied ? 0 : 1) != 0;
     const bool first = uniform(now.first ? 1 : 0) != 0;
     const volatile SegmentInfo& info = sh.segments[now.seg & 7];
+    const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * S::kImage;
     bool boxed = false;  // the tile comes by tensor copies: every row is a key, every box has its page
     if constexpr (!kDecode) {
-      if (boxes > 0) {
+      if (boxes > 0 && direct) {
         const bool mine_ok = mine != nullptr || lane < R::kRows || lane >= R::kRows + boxes;
         boxed = now.whole && __all_sync(0xffffffffu, mine_ok) != 0;
       }
@@ -882,7 +879,7 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
           if (extra != 0) tensor_copy(dst + S::kPeSlab * kSlabBytes, map, S::kPeSlab * kX, mine_row, full);
         }
         __syncwarp();
-      } else {
+      } else if (direct) {
         if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = mine != nullptr ? 1 : 0;
         if constexpr (kDecode) {
           store_half<FMT>(raw, h, row0, lane,
@@ -896,6 +893,20 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* m
         }
         __syncwarp();
         if (lane == 0) arrive(full);
+      } else if (warp == 0) {
+        if (elect_one()) {
+          constexpr uint32_t kHalf = S::kHalfSlabs * kSlabBytes;
+          if (kArrive > 1) arrive(full, kArrive - 1);
+          arrive_expect(full, kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
+          bulk_copy(base + h * kHalf, image + h * kHalf, kHalf, full);
+          if (h == 0) {
+            bulk_copy(base + S::kPeSlab * kSlabBytes, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
+            bulk_copy(smem_u32(sh.valid[st]), image + S::kTile, kKeys, full);
+          }
+        }
+        __syncwarp();
+      } else {
+        if (lane == 0) arrive(full, kArrive);
       }
       if (h == 0 && first && now.seg > 1) {
         // the segment's q rows, once the previous segment's scores have been computed
@@ -1083,24 +1094,14 @@ __device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh
   (void)warp_wait(smem_u32(&sh.bars.drained), 0u, &sh.never);
 }
 
-// An arrival on the pair leader's barrier (this CTA's at the same place).
-__device__ __forceinline__ void arrive_leader(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
 // The softmax of WARPS warps.  A thread has one row (TMEM lane), and of a tile's
 // scores half `half` of the keys, of that (8 warps) half `sub`; of the sums the
-// same half of each 256 columns and half `sub` of the TMEM columns.  PAIR: a
-// step's 128 keys, and the MMA warp's barriers are the leader's.
-template <int OP, int WARPS, bool PAIR, class SharedT>
-__device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, SharedT& sh, uint32_t sP, uint32_t tmem,
-                                             float scale2, int rank = 0) {
-  constexpr int kN = (PAIR ? 256 : 128) / WARPS;  // keys of a thread: 32 or 16
-  constexpr int kParts = WARPS / 2;               // threads to a row
+// same half of each 256 columns and half `sub` of the TMEM columns.
+template <int OP, int WARPS>
+__device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared& sh, uint32_t sP, uint32_t tmem,
+                                             float scale2) {
+  constexpr int kN = 32 * 4 / WARPS;           // keys of a thread: 32 or 16
+  constexpr int kParts = WARPS / 2;            // threads to a row
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const int r = (warp & 1) * 32 + lane;
   const int half = (warp >> 1) & 1, sub = warp >> 2;
@@ -1109,28 +1110,16 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
   const bool negative = scale2 < 0.0f;  // then the scores change sign, and the scale
   scale2 = fabsf(scale2);
   volatile uint32_t* ab = &sh.abort_flag;
-  auto tell = [&](uint64_t* bar) {
-    if constexpr (PAIR) {
-      arrive_leader(smem_u32(bar));
-    } else {
-      arrive(smem_u32(bar));
-    }
-  };
   Segment seg;
   uint32_t it = 0, st = 0, round = 0;
   bool good = true;
-  while (good && next_segment<PAIR>(p, cur, seg, rank)) {
+  while (good && next_segment(p, cur, seg)) {
     float m = -INFINITY;  // the reference maximum of the row, in powers of two
     float l = 0.0f;       // this thread's share of the denominator
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
       const uint32_t buf = it & 1u;
       // the flags first: they are there before the scores, and may have come by the copy engine
-      if constexpr (PAIR) {
-        st = it & 3u;
-        good = warp_wait(smem_u32(&sh.bars.f_full[st]), (it / 4) & 1u, ab) && good;
-      } else {
-        good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab) && good;
-      }
+      good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab) && good;
       uint32_t ok[kN / 4];
 #pragma unroll
       for (int j = 0; j < kN / 16; ++j) {
@@ -1147,11 +1136,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab) && good;
       fence_after();
       uint32_t v[kN];
-      tmem_ld<kN>(tmem + kTmemS + (PAIR ? 64u : 32u) * buf + lanes + static_cast<uint32_t>(sub * kN), v);
+      tmem_ld<kN>(tmem + kTmemS + 32u * buf + lanes + static_cast<uint32_t>(sub * kN), v);
       fence_before();
       __syncwarp();
-      if (lane == 0) tell(&sh.bars.s_empty[buf]);
-      if (!PAIR && ++st == Shape<OP>::kStages) {
+      if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[buf]));
+      if (++st == Shape<OP>::kStages) {
         st = 0;
         ++round;
       }
@@ -1226,7 +1215,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // the weights that were in this buffer have been read
-      constexpr uint32_t kBack = PAIR ? 1 : Shape<OP>::kPBufs;
+      constexpr uint32_t kBack = Shape<OP>::kPBufs;
       if (it >= kBack) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - kBack) & 1u]), ((it - kBack) / 2) & 1u, ab);
       if (moved && !first) {
         // the previous tile's products are in the sums (all threads move or none)
@@ -1254,13 +1243,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < kN / 8; ++j)  // (a pair's weights: a slab for each half of the keys)
-          st_shared(piece_addr(dst, PAIR ? half : 0, r, (PAIR ? sub : part) * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+        for (int j = 0; j < kN / 8; ++j)
+          st_shared(piece_addr(dst, 0, r, part * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
       }
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) tell(&sh.bars.p_full[buf]);
+      if (lane == 0) arrive(smem_u32(&sh.bars.p_full[buf]));
     }
     if (!good) break;
     // ---- the segment's result
@@ -1288,7 +1277,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     }
     fence_before();
     __syncwarp();
-    if (lane == 0) tell(&sh.bars.o_empty);
+    if (lane == 0) arrive(smem_u32(&sh.bars.o_empty));
     sh.xch[part][r] = l;
     bar_sync(2, 32 * WARPS);
     if (part == 0 && keep) {
@@ -1307,17 +1296,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
   }
 }
 
-// Adds up the units' costs: the run of worker `me` of `workers` (CTAs, or pairs of
-// CTAs) among units [first, units), and the unit it starts in.  Thread i takes
-// the n units from first + i n on; plan[slot] gets the length of a run.
-template <class SharedT>
-__device__ __forceinline__ Cursor plan_run(const Params& p, SharedT& sh, int64_t first, int64_t units, int64_t me,
-                                           int64_t workers, int slot) {
-  const int64_t per = (units - first + kThreads - 1) / kThreads;
-  const int64_t u0 = first + static_cast<int64_t>(threadIdx.x) * per;
+// Adds up the units' tiles: this CTA's run of tiles and the unit it starts in.
+// Thread i takes the units [i n, (i + 1) n).
+__device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
+  const int64_t units = static_cast<int64_t>(p.G) + p.T;
+  const int64_t per = (units + kThreads - 1) / kThreads;
+  const int64_t u0 = static_cast<int64_t>(threadIdx.x) * per;
   const int64_t u1 = u0 + per < units ? u0 + per : units;
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
-  int64_t sum = 0, least = 1;
+  int64_t sum = 0;
   bool any_bad = false;
   Unit last{};  // the thread's last unit: its only one as a rule, and then not looked up again
   for (int64_t u = u0; u < u1; ++u) {
@@ -1340,20 +1327,20 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, SharedT& sh, int64_t
     if (w < warp) before += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  // at least a tile's cost, so that every worker between a row tile's first and last has one of its key tiles
-  least = slot == 1 ? kCostStep : p.tile_cost;
-  const int64_t even = (total + workers - 1) / workers, each = even > least ? even : least;
+  // at least a tile's cost, so that every CTA between a row tile's first and last has one of its key tiles
+  const int64_t least = p.tile_cost > p.image_cost ? p.tile_cost : p.image_cost;
+  const int64_t each = (total + p.ctas - 1) / p.ctas > least ? (total + p.ctas - 1) / p.ctas : least;
   Cursor c;
-  c.pos = each * me;
+  c.pos = each * blockIdx.x;
   c.end = c.pos + each < total ? c.pos + each : total;
   int64_t base = before + incl - sum;
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.plan[slot] = each;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.plan[0] = each;
   const bool mine = c.pos >= base && c.pos < base + sum;
   if (mine || blockIdx.x == 0) {
     for (int64_t u = u0; u < u1; ++u) {
       bool bad;
       const Unit x = u + 1 == u1 ? last : unit_at(p, u, bad);
-      if (blockIdx.x == 0) p.plan[2 + u] = base;
+      if (blockIdx.x == 0) p.plan[1 + u] = base;
       if (c.pos >= base && c.pos < base + x.cost()) {
         sh.first_unit = u;
         sh.first_base = base;
@@ -1416,25 +1403,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 32 && p.box_rows > 0)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-  // The lengths, q and the cache rows may come from the upstream kernel.  Behind
-  // the pairs' kernel this one need not wait here: the pairs' waited for all
-  // that, and its CTAs start as the pairs' leave the SMs; it waits at its end,
-  // so that the joining kernel, which waits for this grid's end, sees the pairs'
-  // results too.
-  if (p.image == nullptr) pdl_wait();
-  pdl_trigger();
+  pdl_wait();     // the lengths, q and the cache rows may come from the upstream kernel
+  pdl_trigger();  // the joining kernel waits for this grid's end itself
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(sh.tmem)));
-  // prefixes with decoded tiles are the pairs'
-  const Cursor cur = plan_run(p, sh, p.image != nullptr ? p.G : 0, static_cast<int64_t>(p.G) + p.T, blockIdx.x, p.ctas, 0);
+  const Cursor cur = plan_run(p, sh);
   if (uniform(cur.pos < cur.end ? 1 : 0) != 0) {  // a branch that the compiler sees is uniform
     if (warp < R::kSoft) {
       float scale2 = p.sm_scale * 1.4426950408889634f;  // powers of two: log2(e)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
-      softmax_role<OP, R::kSoft, false>(p, cur, sh, sP, tmem, scale2);
+      softmax_role<OP, R::kSoft>(p, cur, sh, sP, tmem, scale2);
     } else if (warp == R::kMma) {
       mma_role<OP>(p, cur, sh, sQ, sK, sP, tmem);
     } else {
@@ -1447,30 +1428,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
-  if (p.image != nullptr) pdl_wait();
 }
-
-#include "attend_pair.cuh"
 
 // ---- decoded prefix tiles -------------------------------------------------------------
 //
-// A prefix of a group with many rows is read by many pairs of CTAs, 128 rows at
-// a time.  It is decoded once, into tiles as they lie in shared memory (swizzled
-// bf16 values, zeros where there is no key, and a flag for each key), an even
-// number of them; the pairs fetch them by bulk copies.  One block a tile;
-// blocks behind a prefix's end leave.
-template <int FMT>
+// A prefix of a group with many rows is read by many CTAs, 64 rows at a time.
+// It is decoded once, into tiles as they lie in shared memory (swizzled 16-bit
+// values, zeros where there is no key, and a flag for each key); the attention
+// kernel then fetches a tile half with two or three bulk copies.  One block a
+// tile; blocks behind a prefix's end leave.
+template <int FMT, int OP>
 __global__ void __launch_bounds__(256) image_kernel(const Params p) {
   pdl_wait();
-  pdl_trigger();
   const int64_t g = blockIdx.y;
   bool bad;
   const Unit x = unit_at(p, g, bad);
   const int64_t kt = blockIdx.x;
-  if (kt < 2 * x.key_tiles() && x.rows > 0) {
+  if (kt < x.key_tiles() && x.rows > 0) {
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     const int row0 = 8 * warp;
-    uint8_t* dst = p.image + (g * p.image_tiles + kt) * kImage;
+    uint8_t* dst = p.image + (g * p.image_tiles + kt) * Shape<OP>::kImage;
     KeyAt at;
     bool bad_page = false;
     at.fetch(p, x.table, static_cast<int32_t>(x.len), static_cast<int32_t>(kt), row0 + lane, lane < 8);
@@ -1478,7 +1455,7 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
     auto put = [&](int s, int r, int c, const uint4& v) {
       *reinterpret_cast<uint4*>(dst + piece_addr(0, s, r, c)) = v;
     };
-    if constexpr (FMT != MLA_CACHE_BF16) {
+    if constexpr (Roles<FMT, OP>::kDecode) {
       Raw<FMT> raw;
       load_rows<FMT>(raw, mine, lane);
       store_half<FMT>(raw, 0, row0, lane, put);
@@ -1486,13 +1463,14 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        each_piece<kBf16, 8>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+        each_piece<OP, 8>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
           put(s, row0 + r, c, src != nullptr ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0));
         });
     }
-    if (lane < 8) dst[Shape<kBf16>::kTile + row0 + lane] = mine != nullptr ? 1 : 0;
+    if (lane < 8) dst[Shape<OP>::kTile + row0 + lane] = mine != nullptr ? 1 : 0;
     if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
   }
+  pdl_trigger();
 }
 
 // ---- joining a row's segments ----------------------------------------------------------
@@ -1523,8 +1501,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   const bool live = h < p.H;
 
   // the row's segments: n1 of its group's prefix, n2 of its own keys
-  const int64_t each = __ldcg(p.plan), pair_each = __ldcg(p.plan + (p.image != nullptr ? 1 : 0));
-  const int pair = p.image != nullptr ? 2 : 1;  // prefix parts from one worker of a row tile to the next
+  const int64_t each = __ldcg(p.plan);
   int n1 = 0, n2 = 0;
   const uint8_t* part1 = p.prefix_part;  // its first segment of either kind, and the row in it
   const uint8_t* part2 = p.own_part;
@@ -1542,27 +1519,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
       }
       g = lo - 1;
     }
-    // workers c0 .. c1 have the row's key tiles
-    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int64_t run, int64_t& c0, int& n) {
+    // CTAs c0 .. c1 have the row's key tiles
+    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int rows, const uint8_t*& part, int& n) {
       const int64_t per = x.row_cost();
       if (per == 0) return;
-      const int64_t f = __ldcg(p.plan + 2 + unit) + tile * per;
-      c0 = (f + kCostSegment) / run;
-      n = static_cast<int>((f + per - x.tile_cost) / run - c0) + 1;
+      const int64_t f = __ldcg(p.plan + 1 + unit) + tile * per;
+      const int64_t c0 = (f + kCostSegment) / each, c1 = (f + per - x.tile_cost) / each;
+      part += (c0 + x.part0 + tile) * part_bytes(rows);
+      n = static_cast<int>(c1 - c0) + 1;
     };
     bool bad;
-    int64_t c0 = 0;
     const Unit own = unit_at(p, p.G + t, bad);
-    span(own, p.G + t, h / kRowsTile, each, c0, n2);
-    part2 += (c0 + own.part0 + h / kRowsTile) * part_bytes(p.own_rows);
+    span(own, p.G + t, h / kRowsTile, p.own_rows, part2, n2);
     if (g >= 0) {
       const Unit x = unit_at(p, g, bad);
       const int64_t i = t * p.H + h - x.rows0;
       if (i >= 0 && i < x.rows) {
-        c0 = 0;
-        span(x, g, i / x.tile_rows, pair_each, c0, n1);
-        // row tiles of 64 rows: a pair's come two by two
-        part1 += (pair * c0 + x.part0 + i / kRowsTile) * part_bytes(kRowsTile);
+        span(x, g, i / kRowsTile, kRowsTile, part1, n1);
         row1 = static_cast<int>(i % kRowsTile);
       }
     }
@@ -1573,7 +1546,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
     const bool pre = i < n1;
     rows = pre ? kRowsTile : p.own_rows;
     r = pre ? row1 : row2;
-    return pre ? part1 + i * pair * part_bytes(kRowsTile) : part2 + (i - n1) * part_bytes(p.own_rows);
+    return pre ? part1 + i * part_bytes(kRowsTile) : part2 + (i - n1) * part_bytes(p.own_rows);
   };
   auto stats_of = [&](int i, float& m, float& l) {
     int rows, r;
@@ -1692,10 +1665,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
 
 // ---- host ------------------------------------------------------------------------------
 
-// Prefixes go to pairs of CTAs, from tiles decoded into the workspace, when a
-// group has at least kPairRows rows on average and the tiles fit kImageLimit;
-// else they are read from the cache, 64 rows a CTA.
-constexpr int64_t kPairRows = 4 * kRowsTile;
+// A prefix is decoded once, into the workspace, when its rows need decoding (or
+// pages are too small for tensor copies), its group has at least kImageRows rows
+// on average and the images fit kImageLimit; else its tiles are read from the
+// cache.
+constexpr int64_t kImageRows = 4 * kRowsTile;
 constexpr int kLeastBox = 8;  // rows of a tensor copy at least: the swizzle's period
 constexpr int64_t kImageLimit = INT64_C(1) << 31;
 
@@ -1703,19 +1677,19 @@ struct Layout {
   int64_t prefix_part, own_part, image, image_tiles, bytes;
 };
 
+// (The bf16 image's size: the caller need not know which operands a call takes.)
 Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t ctas) {
+  constexpr int64_t kImageBytes = Shape<kBf16>::kImage;
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout l;
-  l.prefix_part = up(8 * (2 + G + T));
-  // row tiles are numbered up to T H / 64 + 2 G, and each worker adds one (a pair two)
-  const int64_t prefix_parts = G > 0 ? T * H / kRowsTile + 2 * G + 2 + ctas : 0;
+  l.prefix_part = up(8 * (1 + G + T));
+  const int64_t prefix_parts = G > 0 ? T * H / kRowsTile + G + 1 + ctas : 0;
   l.own_part = up(l.prefix_part + prefix_parts * part_bytes(kRowsTile));
   const int64_t own_parts = T * ((H + kRowsTile - 1) / kRowsTile) + ctas;
   l.image = up(l.own_part + own_parts * part_bytes(static_cast<int>(H < kRowsTile ? H : kRowsTile)));
-  l.image_tiles = (prefix_keys + 2 * kKeys - 1) / (2 * kKeys) * 2;
-  if (G < 1 || G > 65535 || ctas < 2 || T * H < kPairRows * G || l.image_tiles > kImageLimit / kImage / G)
-    l.image_tiles = 0;
-  l.bytes = up(l.image + G * l.image_tiles * kImage);
+  l.image_tiles = (prefix_keys + kKeys - 1) / kKeys;
+  if (G < 1 || G > 65535 || T * H < kImageRows * G || l.image_tiles > kImageLimit / kImageBytes / G) l.image_tiles = 0;
+  l.bytes = up(l.image + G * l.image_tiles * kImageBytes);
   return l;
 }
 
@@ -1724,13 +1698,14 @@ struct Kernels {
   const void* attend;
   const void* image;
   uint32_t smem;
-  int32_t tile_cost;
+  int32_t image_bytes, tile_cost, image_cost;
 };
 
 template <int FMT, int OP>
 Kernels kernels_of(int32_t tile_cost) {
   return Kernels{reinterpret_cast<const void*>(&attend_kernel<FMT, OP>),
-                 reinterpret_cast<const void*>(&image_kernel<FMT>), Shape<OP>::kSmem, tile_cost};
+                 reinterpret_cast<const void*>(&image_kernel<FMT, OP>), Shape<OP>::kSmem,
+                 static_cast<int32_t>(Shape<OP>::kImage), tile_cost, OP == kF8 ? kCostF8 : kCostImage};
 }
 
 const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kernels_of<MLA_CACHE_E4M3, kBf16>(kCostCodes),
@@ -1738,17 +1713,7 @@ const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kerne
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-std::atomic<bool> g_smem_ready[kMaxDevices][5];  // by kernel; 4: the pairs'
-
-// The shared-memory opt-in of kernel `k` on device `dev` (idempotent: two threads
-// racing here both set the same attribute).
-mla_status smem_ready(int dev, int k, const void* fn, uint32_t bytes) {
-  if (g_smem_ready[dev][k].load(std::memory_order_acquire)) return MLA_OK;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e != cudaSuccess) return cuda_failure(e);
-  g_smem_ready[dev][k].store(true, std::memory_order_release);
-  return MLA_OK;
-}
+std::atomic<bool> g_smem_ready[kMaxDevices][4];
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
@@ -1892,9 +1857,16 @@ mla_status mla_prefix_attend_launch(
 
   const int k = format == MLA_CACHE_E4M3 && q8 ? 3 : format;
   const Kernels& ks = kKernels[k];
+  p.image_bytes = ks.image_bytes;
   p.tile_cost = ks.tile_cost;
-  s = smem_ready(dev, k, ks.attend, ks.smem);
-  if (s != MLA_OK) return s;
+  p.image_cost = ks.image_cost;
+  if (!g_smem_ready[dev][k].load(std::memory_order_acquire)) {
+    // idempotent: two threads racing here both set the same attribute
+    const cudaError_t e =
+        cudaFuncSetAttribute(ks.attend, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ks.smem));
+    if (e != cudaSuccess) return mla::cuda_failure(e);
+    g_smem_ready[dev][k].store(true, std::memory_order_release);
+  }
   // Tensor copies: rows of 16-bit values or codes as they are, in pages of a multiple of eight rows
   CUtensorMap map{};
   p.box_rows = 0;
@@ -1915,22 +1887,16 @@ mla_status mla_prefix_attend_launch(
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return MLA_ERR_INVALID_ARG;
     p.box_rows = box;
+    p.image = nullptr;
   }
   void* args[] = {&p};
   void* attend_args[] = {&map, &p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;
   if (p.image != nullptr) {
-    s = smem_ready(dev, 4, reinterpret_cast<const void*>(&pair_kernel), kPairSmem);
-    if (s != MLA_OK) return s;
     s = launch(ks.image, dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
                args);
     if (s != MLA_OK) return s;
     pdl = true;
-    int32_t e4m3 = format == MLA_CACHE_E4M3 ? 1 : 0;
-    void* pair_args[] = {&p, &e4m3};
-    s = launch(reinterpret_cast<const void*>(&pair_kernel), dim3(static_cast<unsigned>(sms / 2 * 2), 1, 1), kThreads,
-               kPairSmem, pdl, stream, pair_args);
-    if (s != MLA_OK) return s;
   }
   s = launch(ks.attend, dim3(static_cast<unsigned>(sms), 1, 1), kThreads, ks.smem, pdl, stream, attend_args);
   if (s != MLA_OK) return s;
