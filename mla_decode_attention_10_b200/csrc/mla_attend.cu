@@ -91,12 +91,13 @@ template <int FMT, int OP>
 struct Roles {
   static constexpr bool kDecode = OP == kBf16 && FMT != MLA_CACHE_BF16;
   static constexpr int kSoft = kDecode ? 4 : 8;
-  static constexpr int kMma = kSoft;
-  static constexpr int kLoad0 = kSoft + 1;
+  static constexpr int kScores = kSoft;       // the warp that issues the scores' products
+  static constexpr int kSums = kSoft + 1;     // and the sums'
+  static constexpr int kLoad0 = kSoft + 2;
   static constexpr int kLoad = kDecode ? 8 : 4;
   static constexpr int kRows = kRowsTile / kLoad;           // rows of a loader warp
 };
-constexpr int kThreads = 32 * 13;
+constexpr int kThreads = 32 * 14;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
@@ -412,45 +413,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Which of six phases have completed, as bits.  One lane asks (32 lanes' asking
-// costs 32 times as much of the shared-memory pipe) for all six at once, so that
-// a round of the MMA warp costs one trip to shared memory.
-__device__ __forceinline__ uint32_t ask(const uint32_t (&bar)[6], const uint32_t (&parity)[6]) {
-  uint32_t bits;
-  asm volatile(
-      "{\n\t.reg .pred q, p0, p1, p2, p3, p4, p5;\n\t"
-      ".reg .b32 a, b, c;\n\t"
-      "setp.ne.b32 p0, 0, 0;\n\t"
-      "setp.ne.b32 p1, 0, 0;\n\t"
-      "setp.ne.b32 p2, 0, 0;\n\t"
-      "setp.ne.b32 p3, 0, 0;\n\t"
-      "setp.ne.b32 p4, 0, 0;\n\t"
-      "setp.ne.b32 p5, 0, 0;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p0, [%1], %7;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p1, [%2], %8;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p2, [%3], %9;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p3, [%4], %10;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p4, [%5], %11;\n\t"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p5, [%6], %12;\n\t"
-      "selp.u32 a, 1, 0, p0;\n\t"
-      "selp.u32 b, 2, 0, p1;\n\t"
-      "or.b32 a, a, b;\n\t"
-      "selp.u32 b, 4, 0, p2;\n\t"
-      "selp.u32 c, 8, 0, p3;\n\t"
-      "or.b32 b, b, c;\n\t"
-      "or.b32 a, a, b;\n\t"
-      "selp.u32 b, 16, 0, p4;\n\t"
-      "selp.u32 c, 32, 0, p5;\n\t"
-      "or.b32 b, b, c;\n\t"
-      "or.b32 %0, a, b;\n\t}"
-      : "=r"(bits)
-      : "r"(bar[0]), "r"(bar[1]), "r"(bar[2]), "r"(bar[3]), "r"(bar[4]), "r"(bar[5]), "r"(parity[0]), "r"(parity[1]),
-        "r"(parity[2]), "r"(parity[3]), "r"(parity[4]), "r"(parity[5])
-      : "memory");
-  return __reduce_or_sync(0xffffffffu, bits);
-}
-
 // Waits for the phase, at most kWaitSpins tries or until another role gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   for (uint32_t i = 0; i < kWaitSpins; ++i) {
@@ -552,7 +514,7 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2], o_empty;  // [tile & 1]
-  uint64_t drained;
+  uint64_t drained[2];
 };
 
 struct SegmentInfo {
@@ -998,100 +960,86 @@ __device__ __forceinline__ void qk_slabs(uint64_t q, uint64_t k, uint32_t d) {
   }
 }
 
+// Products issued by this warp have completed before TMEM is freed.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t* never) {
+  commit(smem_u32(bar));
+  (void)warp_wait(smem_u32(bar), 0u, never);
+}
+
+// On a wait that ran out (not on another role's): says so, and that all roles stop.
+__device__ __forceinline__ void give_up(const Params& p, uint32_t* abort_flag) {
+  volatile uint32_t* ab = abort_flag;
+  if ((threadIdx.x & 31u) == 0u && *ab == 0u) {
+    *ab = 1u;
+    report(p.status, MLA_STATUS_TIMEOUT);
+  }
+}
+
+// Issues the scores' products of every tile.
 template <int OP>
-__device__ __forceinline__ void mma_role(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK, uint32_t sP,
-                                         uint32_t tmem) {
+__device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK,
+                                             uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
-  const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
-  uint32_t s = 0, v = 0;        // the next tile to get scores, and sums: v <= s <= v + 2
-  uint32_t s_st = 0, s_round = 0, v_st = 0;  // their stages, s's round
-  bool begun = false;           // tile s has its first half's scores
-  uint32_t seg = 0;             // segments begun
-  int left = 0;                 // tiles of the current segment without scores
-  bool more = true, first = false;
-  uint32_t first_bits = 0;      // bit (i & 1): tile i is its segment's first
-  uint32_t v_seg = 0;           // segments whose sums have begun
-  uint32_t idle = 0;
-  // Whichever has its operands goes: the sums of the oldest tile (they free its
-  // stage), else the scores of the next.  Waiting for a certain one of the two
-  // would let the loaders and the tensor cores wait for each other in turn.
+  uint32_t it = 0, st = 0, round = 0, segs = 0;
   while (true) {
-    if (left == 0 && more) {
-      Segment x;
-      left = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
-      more = left > 0;
-      first = true;
-      if (more) ++seg;
-    }
-    if (left == 0 && v == s) break;
-    const uint32_t s_buf = s & 1u;
-    const uint32_t bars[6] = {smem_u32(&sh.bars.p_full[v & 1u]),   smem_u32(&sh.bars.o_empty),
-                              smem_u32(&sh.bars.kv_full[s_st][0]), smem_u32(&sh.bars.kv_full[s_st][1]),
-                              smem_u32(&sh.bars.q_full),           smem_u32(&sh.bars.s_empty[s_buf])};
-    const uint32_t parities[6] = {(v / 2) & 1u, (v_seg - 1) & 1u, s_round & 1u,
-                                  s_round & 1u, (seg - 1) & 1u,   (s / 2 - 1) & 1u};
-    const uint32_t got = ask(bars, parities);
-    const bool opens = ((first_bits >> (v & 1u)) & 1u) != 0u;
-    if (v < s && (got & 1u) != 0u && (!opens || v_seg == 0 || (got & 2u) != 0u)) {
-      fence_after();
-      const uint64_t vd = dV + v_st * (S::kTile >> 4);
-      const uint64_t pd = dP + (S::kPBufs > 1 ? (v & 1u) * (S::kP >> 4) : 0u);
-      if (opens) {
-        pv_products<OP, true>(sh, pd, vd, tmem, v_st, v & 1u);
-        ++v_seg;
-      } else {
-        pv_products<OP, false>(sh, pd, vd, tmem, v_st, v & 1u);
-      }
-      ++v;
-      v_st = v_st + 1 == S::kStages ? 0 : v_st + 1;
-      idle = 0;
-      continue;
-    }
-    const uint32_t d = tmem + kTmemS + 32u * s_buf;
-    const uint64_t k = dK + s_st * (S::kTile >> 4);
-    bool went = false;
-    if (left > 0 && !begun && s < v + 2 && (got & 4u) != 0u && (!first || (got & 16u) != 0u) &&
-        (s < 2 || (got & 32u) != 0u)) {
+    Segment x;
+    const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
+    if (tiles == 0) return true;
+    if (!warp_wait(smem_u32(&sh.bars.q_full), segs & 1u, ab)) return false;
+    ++segs;
+    for (int i = 0; i < tiles; ++i, ++it) {
+      const uint32_t buf = it & 1u, d = tmem + kTmemS + 32u * buf;
+      const uint64_t k = dK + st * (S::kTile >> 4);
+      if (it >= 2 && !warp_wait(smem_u32(&sh.bars.s_empty[buf]), (it / 2 - 1) & 1u, ab)) return false;
+      if (!warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab)) return false;
       fence_async();  // rows that came by plain asynchronous copies, before the tensor cores read them
       fence_after();
       qk_slabs<OP, S::kPeSlab, S::kPeSteps, true>(dQ, k, d);
       qk_slabs<OP, 0, 4 * S::kHalfSlabs, false>(dQ, k, d);
-      begun = went = true;
-    }
-    if (begun && (got & 8u) != 0u) {
+      if (!warp_wait(smem_u32(&sh.bars.kv_full[st][1]), round & 1u, ab)) return false;
       fence_async();
       fence_after();
       qk_slabs<OP, S::kHalfSlabs, 4 * S::kHalfSlabs, false>(dQ, k, d);
-      commit(smem_u32(&sh.bars.s_full[s_buf]));
-      --left;
-      if (left == 0) commit(smem_u32(&sh.bars.q_empty));
-      first_bits = (first_bits & ~(1u << s_buf)) | ((first ? 1u : 0u) << s_buf);
-      first = false;
-      begun = false;
-      went = true;
-      ++s;
-      if (++s_st == S::kStages) {
-        s_st = 0;
-        ++s_round;
+      commit(smem_u32(&sh.bars.s_full[buf]));
+      if (++st == S::kStages) {
+        st = 0;
+        ++round;
       }
     }
-    if (went) {
-      idle = 0;
-      continue;
-    }
-    if (++idle > kWaitSpins || ((idle & 15u) == 15u && __any_sync(0xffffffffu, *ab != 0u))) {
-      if ((threadIdx.x & 31u) == 0u && *ab == 0u) {
-        *ab = 1u;
-        report(p.status, MLA_STATUS_TIMEOUT);
+    commit(smem_u32(&sh.bars.q_empty));
+  }
+}
+
+// Issues the sums' products of every tile.
+template <int OP>
+__device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& sh, uint32_t sK, uint32_t sP,
+                                           uint32_t tmem) {
+  using S = Shape<OP>;
+  volatile uint32_t* ab = &sh.abort_flag;
+  const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
+  uint32_t it = 0, st = 0, segs = 0;
+  while (true) {
+    Segment x;
+    const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
+    if (tiles == 0) return true;
+    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.o_empty), (segs - 1) & 1u, ab)) return false;
+    ++segs;
+    for (int i = 0; i < tiles; ++i, ++it) {
+      const uint32_t buf = it & 1u;
+      if (!warp_wait(smem_u32(&sh.bars.p_full[buf]), (it / 2) & 1u, ab)) return false;
+      fence_async();
+      fence_after();
+      const uint64_t v = dV + st * (S::kTile >> 4), w = dP + (S::kPBufs > 1 ? buf * (S::kP >> 4) : 0u);
+      if (i == 0) {
+        pv_products<OP, true>(sh, w, v, tmem, st, buf);
+      } else {
+        pv_products<OP, false>(sh, w, v, tmem, st, buf);
       }
-      break;
+      if (++st == S::kStages) st = 0;
     }
   }
-  // every product issued has completed before TMEM is freed
-  commit(smem_u32(&sh.bars.drained));
-  (void)warp_wait(smem_u32(&sh.bars.drained), 0u, &sh.never);
 }
 
 // The softmax of WARPS warps.  A thread has one row (TMEM lane), and of a tile's
@@ -1369,7 +1317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = (smem_u32(dsmem) + 1023u) & ~1023u;
   const uint32_t sK = sQ + S::kTile;
   const uint32_t sP = sK + S::kStages * S::kTile;
-  if (warp == R::kMma) {
+  if (warp == R::kScores) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -1398,7 +1346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(&sh.bars.q_full, 32 * R::kLoad);
     init(&sh.bars.q_empty, 1);
     init(&sh.bars.o_empty, R::kSoft);
-    init(&sh.bars.drained, 1);
+    init(&sh.bars.drained[0], 1);
+    init(&sh.bars.drained[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (threadIdx.x == 32 && p.box_rows > 0)
@@ -1416,15 +1365,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
       softmax_role<OP, R::kSoft>(p, cur, sh, sP, tmem, scale2);
-    } else if (warp == R::kMma) {
-      mma_role<OP>(p, cur, sh, sQ, sK, sP, tmem);
+    } else if (warp == R::kScores) {
+      if (!issue_scores<OP>(p, cur, sh, sQ, sK, tmem)) give_up(p, &sh.abort_flag);
+      drain(&sh.bars.drained[0], &sh.never);
+    } else if (warp == R::kSums) {
+      if (!issue_sums<OP>(p, cur, sh, sK, sP, tmem)) give_up(p, &sh.abort_flag);
+      drain(&sh.bars.drained[1], &sh.never);
     } else {
       loader<FMT, OP>(p, &map, cur, sh, sQ, sK);
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == R::kMma) {
+  if (warp == R::kScores) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
