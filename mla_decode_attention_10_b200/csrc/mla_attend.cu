@@ -64,25 +64,60 @@ constexpr uint32_t kSlabBytes = 64 * 128;  // one 128-byte column slab of 64 row
 // each takes three of the weight's bits, nine in all against bf16's eight).
 enum Op { kBf16 = 0, kF8 = 1 };
 
-// A tile in shared memory: 128-byte slabs of its rows, the 512 values first, then
-// the rotary slab (in kF8 half full).  It is filled, used and freed in two
-// halves: the first half of the values with the rotary slab, and the rest.
+// A key tile is 128-byte slabs of its rows: the 512 values, then the rotary slab
+// (in kF8 half full).  In shared memory it lies in two halves of a ring of
+// halves, which are filled, used and freed one by one, and its rotary slab, which
+// comes with the first half, in a slot of its own.  A segment's q rows pass
+// through the ring like a tile, on their way to TMEM; what has no room there
+// (bf16: the last two value slabs and the rotary slab) stays in shared memory.
+// Freed of the q rows, shared memory holds 2.5 tiles instead of 2, or in kF8 4.5
+// instead of 3.
 template <int OP>
 struct Shape {
   static constexpr int kElem = OP == kF8 ? 1 : 2;
   static constexpr int kHalfSlabs = OP == kF8 ? 2 : 4;
   static constexpr int kPeSlab = 2 * kHalfSlabs;
   static constexpr int kPeSteps = OP == kF8 ? 2 : 4;        // MMAs over the rotary slab, 32 bytes of a row each
+  static constexpr int kQSlab0 = OP == kF8 ? kPeSlab + 1 : 6;  // q slabs from here on stay in shared memory
+  static constexpr int kQSlabs = kPeSlab + 1 - kQSlab0;
   static constexpr int kTerms = OP == kF8 ? 3 : 1;          // weights
   static constexpr int kKeySteps = OP == kF8 ? 2 : 4;       // MMAs over a tile's keys, 32 or 16 keys each
-  static constexpr uint32_t kTile = (kPeSlab + 1) * kSlabBytes;          // 72 or 40 KB
+  static constexpr uint32_t kHalf = kHalfSlabs * kSlabBytes;
+  static constexpr int kHalves = OP == kF8 ? 9 : 5;
+  // A tile's first half follows, in its place, the second half of the tile kSlots
+  // before: that tile's rotary slab and flags have been used by then.
+  static constexpr int kSlots = (kHalves + 1) / 2;
   static constexpr uint32_t kP = OP == kF8 ? 2 * kSlabBytes : kSlabBytes;
-  static constexpr int kPBufs = OP == kF8 ? 2 : 1;          // (bf16 has no room for a second)
-  static constexpr int kStages = OP == kF8 ? 3 : 2;
-  static constexpr uint32_t kSmem = kTile * (1 + kStages) + kP * kPBufs + 1024;
-  static constexpr uint32_t kImage = kTile + 128;           // a decoded tile as it lies in shared memory, then its 64 flags
+  static constexpr int kPBufs = OP == kF8 ? 2 : 1;
+  static constexpr uint32_t kPeAt = kHalves * kHalf;
+  static constexpr uint32_t kQAt = kPeAt + kSlots * kSlabBytes;
+  static constexpr uint32_t kPAt = kQAt + kQSlabs * kSlabBytes;
+  static constexpr uint32_t kSmem = kPAt + kP * kPBufs + 1024;
+  static constexpr uint32_t kTile = (kPeSlab + 1) * kSlabBytes;
+  static constexpr uint32_t kImage = kTile + 128;           // a tile as it lies in shared memory, then its 64 flags
 };
-constexpr int kMaxStages = 3;
+constexpr int kMaxHalves = 9, kMaxSlots = 5;
+
+// A role's place in the ring: the half it is at, how often it has been round, and
+// the tile's rotary slot.
+template <int OP>
+struct Ring {
+  uint32_t half = 0, lap = 0, slot = 0;
+  __device__ __forceinline__ void next_half() {
+    if (++half == Shape<OP>::kHalves) {
+      half = 0;
+      ++lap;
+    }
+  }
+  __device__ __forceinline__ void next_tile() {  // both halves passed
+    if (++slot == Shape<OP>::kSlots) slot = 0;
+  }
+  __device__ __forceinline__ void skip_tile() {
+    next_half();
+    next_half();
+    next_tile();
+  }
+};
 
 // Roles.  Rows that need no decoding come by asynchronous copies, which four
 // warps issue easily, and leave eight warps for the softmax; decoding rows
@@ -91,23 +126,29 @@ template <int FMT, int OP>
 struct Roles {
   static constexpr bool kDecode = OP == kBf16 && FMT != MLA_CACHE_BF16;
   static constexpr int kSoft = kDecode ? 4 : 8;
-  static constexpr int kScores = kSoft;       // the warp that issues the scores' products
-  static constexpr int kSums = kSoft + 1;     // and the sums'
-  static constexpr int kLoad0 = kSoft + 2;
+  static constexpr int kLoad0 = kSoft;
   static constexpr int kLoad = kDecode ? 8 : 4;
+  static constexpr int kScores = 12;          // the warp that issues the scores' products
+  static constexpr int kSums = 13;            // and the sums'
+  static constexpr int kLoadRegs = kDecode ? 152 : 176;     // with kIssueRegs and the softmax's 128: 512 for four times four warps
   static constexpr int kRows = kRowsTile / kLoad;           // rows of a loader warp
 };
-constexpr int kThreads = 32 * 14;
+// Sixteen warps (two without work) of 128 registers; the last four hand on to the loaders
+// what issuing products does not need.
+constexpr int kThreads = 32 * 16;
+constexpr int kIssueRegs = 80;
+constexpr uint32_t kArrivals = 33;     // a loader warp's on a half's barrier: its own and its threads' copies'
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
+constexpr uint32_t kTmemQ = 320;       // q rows: 32 bytes of each in 8 columns
 constexpr uint32_t kWaitSpins = 1u << 22;
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
 // What the deal counts (measured cycles, in hundreds): a key tile, by how it
 // comes, and a segment's start and end.
-constexpr int kCostImage = 30, kCostRows = 36, kCostCodes = 60, kCostF8 = 22, kCostSegment = 70;
+constexpr int kCostImage = 23, kCostRows = 25, kCostE4m3 = 66, kCostMx = 80, kCostF8 = 20, kCostSegment = 90;
 
 struct Params {
   const uint8_t* q;
@@ -310,15 +351,15 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn) {
 // registers.  Issued from a branch on the lane, each MMA first moved its
 // descriptors there: 50 to 65 cycles, where the N = 64 form takes 32 (the 4 KB
 // of its operands at 128 bytes a cycle).
-template <int OP, bool ACCUMULATE>
-__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+template <int OP>
+__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (OP == kBf16) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
   } else {
     asm volatile(
@@ -326,9 +367,42 @@ __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint3
         "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@q tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
   }
+}
+
+// The same with A in TMEM.
+template <int OP>
+__device__ __forceinline__ void mma_ws_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (OP == kBf16) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// 16 bytes of each of 64 rows to four columns of TMEM lanes 0..63 and again of
+// lanes 64..127: a .ws product reads its A rows in both places.
+__device__ __forceinline__ void tmem_copy(uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.cp.cta_group::1.64x128b.warpx2::02_13 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc)
+      : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -454,13 +528,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// Two fp16 -> two e5m2 (ties to even), in the low half; and back.
-__device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t c) { return __byte_perm(c, 0u, 0x1404); }
+// Two fp16 rounded to the nearest e5m2 (ties away from zero), as fp16: an e5m2 is
+// the upper byte of an fp16.  Integer arithmetic, since conversions share a unit of
+// a quarter of the rate with the exponentials.  (No finite value here is near
+// e5m2's largest; a NaN may turn into 0, but the row's denominator is a NaN then.)
+__device__ __forceinline__ uint32_t near_e5m2(uint32_t h) { return (h + 0x00800080u) & 0xff00ff00u; }
 
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -505,13 +577,22 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The same of several slabs, each 64 rows below the one before it: a half of a tile at once.
+__device__ __forceinline__ void tensor_copy_half(uint32_t dst, const CUtensorMap* map, int row, int slab, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(slab), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 struct Bars {
-  uint64_t kv_full[kMaxStages][2], kv_empty[kMaxStages][2];
-  uint64_t q_full, q_empty;
+  uint64_t full[kMaxHalves], empty[kMaxHalves];
+  uint64_t q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2], o_empty;  // [tile & 1]
   uint64_t drained[2];
@@ -528,7 +609,7 @@ struct Shared {
   uint32_t tmem;
   uint32_t abort_flag;
   uint32_t never;  // stays 0
-  alignas(16) uint8_t valid[kMaxStages][kKeys];  // 1: the key counts, by stage
+  alignas(16) uint8_t valid[kMaxSlots][kKeys];  // 1: the key counts, by rotary slot
   float xch[4][kRowsTile];
   int64_t warp_sum[kThreads / 32];
   int64_t first_unit, first_base;
@@ -585,28 +666,40 @@ struct Raw {
   uint4 scales;  // mx: the 16 scale bytes of row `lane` (lanes 0..7)
 };
 
+// 16 bytes, or zeros where there is no row; a predicate, not a branch, so that one
+// load need not have come before the next is issued.
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int at) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.s64 p, %4, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%5];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(row), "l"(row + at)
+      : "memory");
+  return v;
+}
+
 template <int FMT>
 __device__ __forceinline__ void load_rows(Raw<FMT>& raw, const uint8_t* mine, int lane) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint8_t* rows[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint8_t* row = row_at(mine, 2 * j + (lane >> 4));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      raw.codes[4 * h + j] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row) + 16 * h + (lane & 15)) : zero;
-    }
-  }
+  for (int j = 0; j < 4; ++j) rows[j] = row_at(mine, 2 * j + (lane >> 4));
   if constexpr (FMT == MLA_CACHE_MX) {
-    raw.scales = mine != nullptr ? __ldcg(reinterpret_cast<const uint4*>(mine + kMxScales)) : zero;
+    const uint8_t* rest[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* row = row_at(mine, 4 * i + (lane >> 3));
-      raw.rest[i] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row + kMxPe) + (lane & 7)) : zero;
-    }
+    for (int i = 0; i < 2; ++i) rest[i] = row_at(mine, 4 * i + (lane >> 3));
+    raw.scales = load16(mine, kMxScales);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) raw.rest[i] = load16(rest[i], kMxPe + 16 * (lane & 7));
   } else {
-    const uint8_t* row = row_at(mine, lane >> 2);
-    raw.rest[0] = row != nullptr ? __ldcg(reinterpret_cast<const uint4*>(row) + 32 + (lane & 3)) : zero;
+    raw.rest[0] = load16(row_at(mine, lane >> 2), 512 + 16 * (lane & 3));
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw.codes[4 * h + j] = load16(rows[j], 256 * h + 16 * (lane & 15));
 }
 
 // Sixteen codes -> two pieces of bf16 values.
@@ -655,36 +748,37 @@ __device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0,
 
 // ---- the roles ---------------------------------------------------------------------
 
-// A walk over this CTA's key tiles, one at a time.
+// A walk over this CTA's key tiles, one at a time.  A tile that comes by copies of
+// many bytes each (an image's, or a whole one by tensor copies) is one loader
+// warp's work, in turn; of the others each warp has some rows.
 struct TileWalk {
   Cursor cur;
   const int32_t* table;
-  int32_t len, kt, k1;
-  int32_t seg;   // segments begun
-  bool copied;   // the segment's tiles come from an image
-  bool first;    // the tile is its segment's first
-  bool any;      // not yet behind the last
+  int32_t len, kt, k0, k1;
+  int32_t seg;     // segments begun
+  int32_t owned;   // tiles of the segment before this one are one warp's each
+  bool copied;     // the segment's tiles come from an image
+  bool any;        // not yet behind the last
 
   __device__ __forceinline__ void start(const Cursor& c) {
     cur = c;
-    kt = k1 = seg = len = 0;
+    kt = k0 = k1 = seg = len = owned = 0;
     table = nullptr;
-    copied = first = false;
+    copied = false;
     any = true;
   }
-  // To the next tile.
-  __device__ __forceinline__ void next(const Params& p, Shared& sh) {
-    if (!any) return;
-    first = ++kt >= k1;
-    if (!first) return;
+  // To the next tile.  `boxes`: tensor copies are made.
+  __device__ __forceinline__ void next(const Params& p, Shared& sh, bool boxes) {
+    if (!any || ++kt < k1) return;
     Segment s;
-    any = next_segment(p, cur, s);
+    any = uniform(next_segment(p, cur, s) ? 1 : 0) != 0;
     if (!any) return;
     table = s.table;
     len = static_cast<int32_t>(s.len);
-    kt = s.k0;
+    kt = k0 = s.k0;
     k1 = s.k1;
     copied = s.image != nullptr;
+    owned = copied ? k1 : boxes ? len / kKeys : 0;
     ++seg;
     // Kept for the tiles' own turn.  Every loader warp writes the same values;
     // they are at most 2 + 2 + 1 segments apart, so none is overwritten too early.
@@ -697,10 +791,18 @@ struct TileWalk {
 
 struct Tile {
   int32_t kt, seg;
-  bool copied, first, any, whole;  // whole: no key behind the sequence's end
+  bool copied, first, any;
+  bool whole;  // one warp's work
+  bool mine;   // this warp has work with it
 
-  __device__ __forceinline__ explicit Tile(const TileWalk& w)
-      : kt(w.kt), seg(w.seg), copied(w.copied), first(w.first), any(w.any), whole(w.kt < w.len / kKeys) {}
+  __device__ __forceinline__ Tile(const TileWalk& w, int warp, int warps)
+      : kt(w.kt),
+        seg(w.seg),
+        copied(w.copied),
+        first(w.kt == w.k0),
+        any(w.any),
+        whole(w.kt < w.owned),
+        mine(!(w.kt < w.owned) || (w.kt - w.k0) % warps == warp) {}
 };
 
 // Where the key of row r of a tile lies.  The page number is fetched a tile
@@ -736,174 +838,228 @@ __device__ __forceinline__ const uint8_t* q_row(const Params& p, int32_t row0, i
   return p.q + static_cast<int64_t>(t) * p.q_st + static_cast<int64_t>(row - t * p.H) * p.q_sh;
 }
 
-// The segment's 64 q rows, by all loader threads; q_full gets one arrival of each.
-template <int FMT, int OP>
-__device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t rows, uint32_t sQ, uint32_t bar, int warp,
-                                       int lane) {
+// A loader warp's part of the segment's 64 q rows, to `to(slab, row, piece)`; the
+// two halves' barriers get the warp's arrivals.
+template <int FMT, int OP, class To>
+__device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t rows, const To& to, uint32_t full0,
+                                       uint32_t full1, int warp, int lane) {
   constexpr int kRows = Roles<FMT, OP>::kRows;
   bool ok;
   const uint8_t* mine = q_row(p, row0, rows, kRows * warp + lane % kRows, ok);
   if (!ok || lane >= kRows) mine = nullptr;
+  uint32_t arrivals = 1;
   if (OP == kBf16 && p.q_fp8) {
 #pragma unroll
     for (int i = 0; i < kRows / 8; ++i) {
       const uint8_t* eight = row_at(mine, 8 * i + (lane & 7));
       Raw<MLA_CACHE_E4M3> raw;
       load_rows<MLA_CACHE_E4M3>(raw, lane < 8 ? eight : nullptr, lane);
-      auto put = [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(sQ, s, r, c), v); };
+      auto put = [&](int s, int r, int c, const uint4& v) { st_shared(to(s, r, c), v); };
       store_half<MLA_CACHE_E4M3>(raw, 0, kRows * warp + 8 * i, lane, put);
       store_half<MLA_CACHE_E4M3>(raw, 1, kRows * warp + 8 * i, lane, put);
     }
     fence_async();
-    __syncwarp();
-    if (lane == 0) arrive(bar, 32);
+    arrivals = kArrivals;
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       each_piece<OP, kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
-        cp_async16(piece_addr(sQ, s, kRows * warp + r, c), src != nullptr ? src : p.q, src != nullptr);
+        cp_async16(to(s, kRows * warp + r, c), src != nullptr ? src : p.q, src != nullptr);
       });
-    cp_async_arrive(bar);
+    cp_async_arrive(full0);
+    cp_async_arrive(full1);
+  }
+  __syncwarp();
+  if (lane == 0) {
+    arrive(full0, arrivals);
+    arrive(full1, arrivals);
   }
 }
 
-// Loader warps fill the stages, tile by tile.  A half's barrier counts one
-// arrival a warp, and where rows come by asynchronous copies one a thread too.
+// The cache as seen by tensor copies: 128 bytes of box_rows rows; and where that is
+// a whole tile, half a tile's slabs of 64 rows.
+struct Maps {
+  const CUtensorMap *slab, *half;
+};
+
+// Loader warps fill the ring: for each segment its q rows, then tile by tile.  A
+// half's barrier counts kArrivals of each warp: one of its own, and one of each
+// thread's asynchronous copies where there are any.
 template <int FMT, int OP>
-__device__ __forceinline__ bool load_tiles(const Params& p, const CUtensorMap* map, const Cursor& cur, Shared& sh,
-                                           uint32_t sQ, uint32_t sK, bool& bad_page) {
+__device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, const Cursor& cur, Shared& sh,
+                                           uint32_t smem, bool& bad_page) {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
   constexpr bool kDecode = R::kDecode;
-  constexpr uint32_t kArrive = kDecode ? 1 : 33;
   const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - R::kLoad0), lane = static_cast<int>(threadIdx.x) & 31;
   const int row0 = R::kRows * warp;
   volatile uint32_t* ab = &sh.abort_flag;
-  // Lane i < kRows looks after row i of the warp's: its page number is fetched
-  // two tiles ahead.  Where tensor copies are made, lane kRows + i looks after
-  // box i of the tile: a tile that is all keys comes by one copy a box and slab.
+  // Of a tile that all warps fill, lane i < kRows looks after row i of the warp's;
+  // of one that comes by tensor copies, lane i after box i, which is copied slab
+  // by slab.  Page numbers are fetched two tiles ahead.
   TileWalk w;  // two tiles ahead of the one being stored
   KeyAt at;
   Raw<kDecode ? FMT : MLA_CACHE_E4M3> raw;
   const int boxes = !kDecode && p.box_rows > 0 ? kKeys / p.box_rows : 0;
-  const int look = lane < R::kRows ? row0 + lane : lane < R::kRows + boxes ? (lane - R::kRows) * p.box_rows : -1;
+  Ring<OP> ring;
+  // the ring's next half, when it is free
+  auto acquire = [&]() { return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, ab); };
+  auto fill_q = [&](int seg) {
+    const volatile SegmentInfo& info = sh.segments[seg & 7];
+    // the previous segment's scores have been computed
+    if (seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab)) return false;
+    const uint32_t full0 = smem_u32(&sh.bars.full[ring.half]), base0 = smem + ring.half * S::kHalf;
+    if (!acquire()) return false;
+    ring.next_half();
+    const uint32_t full1 = smem_u32(&sh.bars.full[ring.half]), base1 = smem + ring.half * S::kHalf;
+    if (!acquire()) return false;
+    ring.next_half();
+    const uint32_t rest = smem + S::kQAt, pe = smem + S::kPeAt + ring.slot * kSlabBytes;
+    ring.next_tile();
+    auto to = [&](int s, int r, int c) {
+      return s >= S::kQSlab0      ? piece_addr(rest, s - S::kQSlab0, r, c)
+             : s == S::kPeSlab    ? piece_addr(pe, 0, r, c)
+             : s >= S::kHalfSlabs ? piece_addr(base1, s - S::kHalfSlabs, r, c)
+                                  : piece_addr(base0, s, r, c);
+    };
+    load_q<FMT, OP>(p, info.row0, info.rows, to, full0, full1, warp, lane);
+    return true;
+  };
   w.start(cur);
-  w.next(p, sh);
-  auto fetch = [&]() { at.fetch(p, w.table, w.len, w.kt, look, w.any && look >= 0 && !w.copied); };
-  Tile now(w);
-  fetch();
+  w.next(p, sh, boxes > 0);
+  Tile now(w, warp, R::kLoad);
+  auto fetch = [&](const Tile& t) {
+    if (!t.any || !t.mine || t.copied) return;
+    const int look = !t.whole ? (lane < R::kRows ? row0 + lane : -1) : lane < boxes ? lane * p.box_rows : -1;
+    at.fetch(p, w.table, w.len, t.kt, look, look >= 0);
+  };
+  // where the tile's rows lie that this lane looks after
+  const uint8_t *mine = nullptr, *mine_next = nullptr;
+  int32_t box = 0, box_next = 0;
+  auto locate = [&](const Tile& t, const uint8_t*& row, int32_t& first) {
+    row = nullptr;
+    if (!t.any || !t.mine || t.copied) return;
+    row = at.address(p, row_bytes(FMT), bad_page);
+    first = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
+  };
+  fetch(now);
   // the first segment's q rows go out while page numbers are under way
-  if (uniform(now.any ? 1 : 0) != 0) {
-    const volatile SegmentInfo& info = sh.segments[now.seg & 7];
-    load_q<FMT, OP>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
+  if (now.any && !fill_q(now.seg)) return false;
+  locate(now, mine, box);
+  if constexpr (kDecode) {
+    if (!now.copied) load_rows<FMT>(raw, mine, lane);
   }
-  const uint8_t* mine = at.address(p, row_bytes(FMT), bad_page);
-  int32_t mine_row = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);  // of a box
-  w.next(p, sh);
-  Tile then(w);
-  fetch();
-  if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
-  uint32_t st = 0, round = 0;  // stage, and how often the stages have been round
-  while (uniform(now.any ? 1 : 0) != 0) {
-    const uint32_t base = sK + st * S::kTile;
-    const bool direct = uniform(now.copied ? 0 : 1) != 0;
-    const bool first = uniform(now.first ? 1 : 0) != 0;
-    const volatile SegmentInfo& info = sh.segments[now.seg & 7];
-    const uint8_t* image = direct ? nullptr : info.image + static_cast<int64_t>(now.kt) * S::kImage;
-    bool boxed = false;  // the tile comes by tensor copies: every row is a key, every box has its page
-    if constexpr (!kDecode) {
-      if (boxes > 0 && direct) {
-        const bool mine_ok = mine != nullptr || lane < R::kRows || lane >= R::kRows + boxes;
-        boxed = now.whole && __all_sync(0xffffffffu, mine_ok) != 0;
-      }
-    }
+  w.next(p, sh, boxes > 0);
+  Tile then(w, warp, R::kLoad);
+  fetch(then);
+  while (now.any) {
+    if (now.first && now.seg > 1 && !fill_q(now.seg)) return false;
+    locate(then, mine_next, box_next);
+    w.next(p, sh, boxes > 0);
+    const Tile after(w, warp, R::kLoad);
+    fetch(after);
+    if (!now.mine) {
+      // waits all the same: a wait tells a phase from the one before, not from the one before that
+      ring.next_half();
+      if (!acquire()) return false;
+      ring.next_half();
+      ring.next_tile();
+    } else {
+      const uint32_t pe = smem + S::kPeAt + ring.slot * kSlabBytes;
+      uint8_t* valid = sh.valid[ring.slot];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t full = smem_u32(&sh.bars.kv_full[st][h]);
-      if (round > 0 && !warp_wait(smem_u32(&sh.bars.kv_empty[st][h]), (round - 1) & 1u, ab)) return false;
-      if (boxed) {
-        if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = 1;
-        __syncwarp();
-        // the half's slabs over the loader warps: issuing one copy takes about 90 cycles
-        constexpr int kSlabs = S::kHalfSlabs;
-        const int extra = h == 0 && warp == kSlabs % R::kLoad ? 1 : 0;  // this warp copies the rotary slab
-        const int mine_slabs = (warp < kSlabs ? 1 : 0) + extra;
-        if (lane == R::kRows) {
-          arrive(full, kArrive - 1);
-          arrive_expect(full, static_cast<uint32_t>(mine_slabs) * kSlabBytes);
-        }
-        __syncwarp();
-        if (lane >= R::kRows && lane < R::kRows + boxes) {
-          const uint32_t dst = base + static_cast<uint32_t>(look) * 128u;
-          constexpr int kX = 128 / S::kElem;
-          const int s = h * kSlabs + warp;
-          if (warp < kSlabs) tensor_copy(dst + static_cast<uint32_t>(s) * kSlabBytes, map, s * kX, mine_row, full);
-          if (extra != 0) tensor_copy(dst + S::kPeSlab * kSlabBytes, map, S::kPeSlab * kX, mine_row, full);
-        }
-        __syncwarp();
-      } else if (direct) {
-        if (h == 0 && lane < R::kRows) sh.valid[st][row0 + lane] = mine != nullptr ? 1 : 0;
-        if constexpr (kDecode) {
-          store_half<FMT>(raw, h, row0, lane,
-                          [&](int s, int r, int c, const uint4& v) { st_shared(piece_addr(base, s, r, c), v); });
-          fence_async();
-        } else {
-          each_piece<OP, R::kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
-            cp_async16(piece_addr(base, s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
-          });
-          cp_async_arrive(full);
-        }
-        __syncwarp();
-        if (lane == 0) arrive(full);
-      } else if (warp == 0) {
-        if (elect_one()) {
-          constexpr uint32_t kHalf = S::kHalfSlabs * kSlabBytes;
-          if (kArrive > 1) arrive(full, kArrive - 1);
-          arrive_expect(full, kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
-          bulk_copy(base + h * kHalf, image + h * kHalf, kHalf, full);
-          if (h == 0) {
-            bulk_copy(base + S::kPeSlab * kSlabBytes, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
-            bulk_copy(smem_u32(sh.valid[st]), image + S::kTile, kKeys, full);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t full = smem_u32(&sh.bars.full[ring.half]), base = smem + ring.half * S::kHalf;
+        if (!acquire()) return false;
+        ring.next_half();
+        auto to = [&](int s, int r, int c) {
+          return s == S::kPeSlab ? piece_addr(pe, 0, r, c) : piece_addr(base, s - h * S::kHalfSlabs, r, c);
+        };
+        if (!now.whole) {
+          if (h == 0 && lane < R::kRows) valid[row0 + lane] = mine != nullptr ? 1 : 0;
+          if constexpr (kDecode) {
+            store_half<FMT>(raw, h, row0, lane, [&](int s, int r, int c, const uint4& v) { st_shared(to(s, r, c), v); });
+          } else {
+            each_piece<OP, R::kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+              cp_async16(to(s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
+            });
+            cp_async_arrive(full);
           }
+          __syncwarp();
+          if (lane == 0) arrive(full, kDecode ? kArrivals : 1);
+        } else if (now.copied) {
+          if (elect_one()) {
+            const volatile SegmentInfo& info = sh.segments[now.seg & 7];
+            const uint8_t* image = info.image + static_cast<int64_t>(now.kt) * S::kImage;
+            arrive(full, kArrivals * R::kLoad - 1);
+            arrive_expect(full, S::kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
+            bulk_copy(base, image + h * S::kHalf, S::kHalf, full);
+            if (h == 0) {
+              bulk_copy(pe, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
+              bulk_copy(smem_u32(valid), image + S::kTile, kKeys, full);
+            }
+          }
+          __syncwarp();
+        } else if constexpr (!kDecode) {
+          // a box in a page that does not exist: no keys
+          const uint32_t gone = __ballot_sync(0xffffffffu, lane < boxes && mine == nullptr);
+          const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+          const int slabs = S::kHalfSlabs + (h == 0 ? 1 : 0);
+          if (h == 0)
+            for (int i = lane; i < kKeys; i += 32) valid[i] = (gone >> (i / p.box_rows)) & 1u ? 0 : 1;
+          if (gone != 0u) {
+            for (int i = lane; i < slabs * kKeys * 8; i += 32) {
+              const int s = i / (kKeys * 8), r = (i >> 3) % kKeys;
+              if ((gone >> (r / p.box_rows)) & 1u)
+                st_shared(to(s < S::kHalfSlabs ? h * S::kHalfSlabs + s : S::kPeSlab, r, i & 7), make_uint4(0, 0, 0, 0));
+            }
+            fence_async();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            arrive(full, kArrivals * R::kLoad - 1);
+            arrive_expect(full, static_cast<uint32_t>(slabs * (boxes - __popc(gone))) * box_bytes);
+          }
+          __syncwarp();
+          if (lane < boxes && mine != nullptr) {
+            constexpr int kX = 128 / S::kElem;
+            const uint32_t row = static_cast<uint32_t>(lane) * box_bytes;
+            if (h == 0) tensor_copy(pe + row, maps.slab, S::kPeSlab * kX, box, full);
+            if (boxes == 1) {
+              tensor_copy_half(base, maps.half, box, h * S::kHalfSlabs, full);
+            } else {
+#pragma unroll
+              for (int s = 0; s < S::kHalfSlabs; ++s)
+                tensor_copy(base + static_cast<uint32_t>(s) * kSlabBytes + row, maps.slab, (h * S::kHalfSlabs + s) * kX, box,
+                            full);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      } else {
-        if (lane == 0) arrive(full, kArrive);
       }
-      if (h == 0 && first && now.seg > 1) {
-        // the segment's q rows, once the previous segment's scores have been computed
-        if (!warp_wait(smem_u32(&sh.bars.q_empty), (now.seg - 2) & 1u, ab)) return false;
-        load_q<FMT, OP>(p, info.row0, info.rows, sQ, smem_u32(&sh.bars.q_full), warp, lane);
-      }
+      ring.next_tile();
     }
-    // the next tile's loads go out behind the fences, which would wait for them
-    mine = at.address(p, row_bytes(FMT), bad_page);
-    mine_row = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
-    if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
+    // Behind the tile's last arrival: an arrival waits for the loads before it.
+    if constexpr (kDecode) load_rows<FMT>(raw, mine_next, lane);
     now = then;
-    w.next(p, sh);
-    then = Tile(w);
-    fetch();
-    if (++st == S::kStages) {
-      st = 0;
-      ++round;
-    }
+    then = after;
+    mine = mine_next;
+    box = box_next;
   }
   return true;
 }
 
 template <int FMT, int OP>
-__device__ __forceinline__ void loader(const Params& p, const CUtensorMap* map, const Cursor& cur, Shared& sh,
-                                       uint32_t sQ, uint32_t sK) {
+__device__ __forceinline__ void loader(const Params& p, const Maps& maps, const Cursor& cur, Shared& sh,
+                                       uint32_t smem) {
   bool bad_page = false;
-  const bool good = load_tiles<FMT, OP>(p, map, cur, sh, sQ, sK, bad_page);
+  const bool good = load_tiles<FMT, OP>(p, maps, cur, sh, smem, bad_page);
   // no copy may be under way when the CTA ends: on the way out after a timeout
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!good) {
-    for (int i = 0; i < 2 * Shape<OP>::kStages; ++i)
-      for (uint32_t parity = 0; parity < 2; ++parity)
-        (void)warp_wait(smem_u32(&sh.bars.kv_full[i >> 1][i & 1]), parity, &sh.never);
+    for (int i = 0; i < Shape<OP>::kHalves; ++i)
+      for (uint32_t parity = 0; parity < 2; ++parity) (void)warp_wait(smem_u32(&sh.bars.full[i]), parity, &sh.never);
   }
   if (!good && (threadIdx.x & 31u) == 0u && *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) == 0u) {
     *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) = 1u;
@@ -912,52 +1068,74 @@ __device__ __forceinline__ void loader(const Params& p, const CUtensorMap* map, 
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
 }
 
-// The products of one tile's weights with its values, into the sums: columns 0..255, then 256..511.
-template <int OP, bool FIRST>
-__device__ __forceinline__ void pv_half(uint64_t p, uint64_t v, uint32_t tmem, int half) {
+// The products of one tile's weights with half of its values, into 256 columns of
+// the sums, which they add to (`more`) or begin.
+template <int OP>
+__device__ __forceinline__ void pv_half(uint64_t p, uint64_t v, uint32_t d, uint32_t more) {
   using S = Shape<OP>;
   constexpr uint32_t id = instr_desc<OP>(256, true);
   constexpr uint64_t kStep = static_cast<uint64_t>(kSlabBytes / S::kKeySteps) >> 4;  // that many keys further down the tile
-  const uint32_t d = tmem + static_cast<uint32_t>(half) * 128u;
-  const uint64_t vh = v + static_cast<uint64_t>(half * S::kHalfSlabs * (kSlabBytes >> 4));
 #pragma unroll
   for (int t = 0; t < S::kTerms; ++t) {
     // weights: 32-byte steps along a row; kF8 terms at bytes 0 and 64 of the first slab, 0 of the second
     const uint64_t pt = p + static_cast<uint64_t>(t == 1 ? 4 : t == 2 ? kSlabBytes >> 4 : 0);
 #pragma unroll
-    for (int j = 0; j < S::kKeySteps; ++j) {
-      if (FIRST && t == 0 && j == 0) {
-        mma_ws<OP, false>(d, pt, vh, id);
-      } else {
-        mma_ws<OP, true>(d, pt + static_cast<uint64_t>(j * 2), vh + static_cast<uint64_t>(j) * kStep, id);
-      }
-    }
+    for (int j = 0; j < S::kKeySteps; ++j)
+      mma_ws<OP>(d, pt + static_cast<uint64_t>(j * 2), v + static_cast<uint64_t>(j) * kStep, id, t == 0 && j == 0 ? more : 1u);
   }
 }
 
-template <int OP, bool FIRST>
-__device__ __forceinline__ void pv_products(Shared& sh, uint64_t p, uint64_t v, uint32_t tmem, uint32_t st,
-                                            uint32_t buf) {
-  pv_half<OP, FIRST>(p, v, tmem, 0);
-  commit(smem_u32(&sh.bars.kv_empty[st][0]));
-  pv_half<OP, FIRST>(p, v, tmem, 1);
-  commit(smem_u32(&sh.bars.kv_empty[st][1]));
-  commit(smem_u32(&sh.bars.pv_done[buf]));
-}
-
-// Scores: MMAs over STEPS 32-byte pieces of the rows from slab S0 on.
-template <int OP, int S0, int STEPS, bool FIRST>
-__device__ __forceinline__ void qk_slabs(uint64_t q, uint64_t k, uint32_t d) {
-  constexpr uint32_t id = instr_desc<OP>(kKeys, false);
+// Scores over `slabs` slabs of the keys at `k` and of the q rows, in TMEM or in
+// shared memory.  (Unrolled over the slabs too, the compiler kept every product's
+// addresses in registers, and where it ran out of them fetched some from memory
+// before each product.)
+template <int OP>
+__device__ __forceinline__ void qk_tmem(uint32_t q, uint64_t k, uint32_t d, int slabs) {
+#pragma unroll 1
+  for (int s = 0; s < slabs; ++s) {
 #pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    const uint64_t off = static_cast<uint64_t>((S0 + (j >> 2)) * (kSlabBytes >> 4) + (j & 3) * 2);
-    if (FIRST && j == 0) {
-      mma_ws<OP, false>(d, q + off, k + off, id);
+    for (int j = 0; j < 4; ++j)
+      mma_ws_tmem<OP>(d, q + 8u * static_cast<uint32_t>(j), k + static_cast<uint64_t>(2 * j), instr_desc<OP>(kKeys, false), 1u);
+    q += 32u;
+    k += kSlabBytes >> 4;
+  }
+}
+
+template <int OP>
+__device__ __forceinline__ void qk_smem(uint64_t q, uint64_t k, uint32_t d, int slabs) {
+#pragma unroll 1
+  for (int s = 0; s < slabs; ++s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      mma_ws<OP>(d, q + static_cast<uint64_t>(2 * j), k + static_cast<uint64_t>(2 * j), instr_desc<OP>(kKeys, false), 1u);
+    q += kSlabBytes >> 4;
+    k += kSlabBytes >> 4;
+  }
+}
+
+// Scores over the rotary slab: the first of a tile.
+template <int OP>
+__device__ __forceinline__ void qk_rotary(uint32_t q_tmem, uint64_t q_smem, uint64_t k, uint32_t d) {
+  using S = Shape<OP>;
+#pragma unroll
+  for (int j = 0; j < S::kPeSteps; ++j) {
+    if constexpr (S::kPeSlab < S::kQSlab0) {
+      mma_ws_tmem<OP>(d, q_tmem + 8u * static_cast<uint32_t>(j), k + static_cast<uint64_t>(2 * j), instr_desc<OP>(kKeys, false),
+                      j > 0 ? 1u : 0u);
     } else {
-      mma_ws<OP, true>(d, q + off, k + off, id);
+      mma_ws<OP>(d, q_smem + static_cast<uint64_t>(2 * j), k + static_cast<uint64_t>(2 * j), instr_desc<OP>(kKeys, false),
+                 j > 0 ? 1u : 0u);
     }
   }
+}
+
+// STEPS 32-byte pieces of the q rows, at `q`, to TMEM from piece J0 on.
+template <int J0, int STEPS>
+__device__ __forceinline__ void q_copy(uint64_t q, uint32_t tmem) {
+#pragma unroll
+  for (int i = 0; i < 2 * STEPS; ++i)
+    tmem_copy(tmem + kTmemQ + 8u * J0 + 4u * static_cast<uint32_t>(i),
+              q + static_cast<uint64_t>((i >> 3) * (kSlabBytes >> 4) + (i & 7)));
 }
 
 // Products issued by this warp have completed before TMEM is freed.
@@ -975,38 +1153,59 @@ __device__ __forceinline__ void give_up(const Params& p, uint32_t* abort_flag) {
   }
 }
 
-// Issues the scores' products of every tile.
+// Issues the copies of every segment's q rows to TMEM and the scores' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared& sh, uint32_t sQ, uint32_t sK,
-                                             uint32_t tmem) {
+__device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
-  const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
-  uint32_t it = 0, st = 0, round = 0, segs = 0;
+  const uint64_t d_half = smem_desc(smem, 16, 1024), d_pe = smem_desc(smem + S::kPeAt, 16, 1024);
+  const uint64_t d_q = smem_desc(smem + S::kQAt, 16, 1024);  // the q rows' slabs from kQSlab0 on
+  const uint32_t q = tmem + kTmemQ;
+  uint32_t it = 0;
+  Ring<OP> ring;
+  // The half has come, and the tensor cores may read it.  (The fence between plain
+  // stores or asynchronous copies and the tensor cores' reads is made here: made by
+  // the warps that decode rows, it waited for the next rows' loads.)
+  auto come = [&]() {
+    if (!warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab)) return false;
+    fence_async();
+    fence_after();
+    return true;
+  };
   while (true) {
     Segment x;
     const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
     if (tiles == 0) return true;
-    if (!warp_wait(smem_u32(&sh.bars.q_full), segs & 1u, ab)) return false;
-    ++segs;
+    // The products that read the previous segment's q rows have completed: the
+    // loaders waited for that.  Those that read these run behind the copies.
+    if (!come()) return false;
+    q_copy<0, 4 * S::kHalfSlabs>(smem_desc(smem + ring.half * S::kHalf, 16, 1024), tmem);
+    if (S::kPeSlab < S::kQSlab0)
+      q_copy<4 * S::kPeSlab, S::kPeSteps>(smem_desc(smem + S::kPeAt + ring.slot * kSlabBytes, 16, 1024), tmem);
+    commit(smem_u32(&sh.bars.empty[ring.half]));
+    ring.next_half();
+    if (!come()) return false;
+    constexpr int kSlabs = (S::kQSlab0 < S::kPeSlab ? S::kQSlab0 : S::kPeSlab) - S::kHalfSlabs;
+    q_copy<4 * S::kHalfSlabs, 4 * kSlabs>(smem_desc(smem + ring.half * S::kHalf, 16, 1024), tmem);
+    commit(smem_u32(&sh.bars.empty[ring.half]));
+    ring.next_half();
+    ring.next_tile();
     for (int i = 0; i < tiles; ++i, ++it) {
-      const uint32_t buf = it & 1u, d = tmem + kTmemS + 32u * buf;
-      const uint64_t k = dK + st * (S::kTile >> 4);
+      const uint32_t buf = it & 1u;
+      const uint32_t d = tmem + kTmemS + 32u * buf;
       if (it >= 2 && !warp_wait(smem_u32(&sh.bars.s_empty[buf]), (it / 2 - 1) & 1u, ab)) return false;
-      if (!warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab)) return false;
-      fence_async();  // rows that came by plain asynchronous copies, before the tensor cores read them
-      fence_after();
-      qk_slabs<OP, S::kPeSlab, S::kPeSteps, true>(dQ, k, d);
-      qk_slabs<OP, 0, 4 * S::kHalfSlabs, false>(dQ, k, d);
-      if (!warp_wait(smem_u32(&sh.bars.kv_full[st][1]), round & 1u, ab)) return false;
-      fence_async();
-      fence_after();
-      qk_slabs<OP, S::kHalfSlabs, 4 * S::kHalfSlabs, false>(dQ, k, d);
+      if (!come()) return false;
+      qk_rotary<OP>(q + 32u * S::kPeSlab, d_q + static_cast<uint64_t>(S::kQSlabs > 0 ? (S::kQSlabs - 1) * (kSlabBytes >> 4) : 0),
+                    d_pe + ring.slot * (kSlabBytes >> 4), d);
+      qk_tmem<OP>(q, d_half + ring.half * (S::kHalf >> 4), d, S::kHalfSlabs);
+      ring.next_half();
+      if (!come()) return false;
+      const uint64_t k = d_half + ring.half * (S::kHalf >> 4);
+      qk_tmem<OP>(q + 32u * S::kHalfSlabs, k, d, kSlabs);
+      if (kSlabs < S::kHalfSlabs) qk_smem<OP>(d_q, k + kSlabs * (kSlabBytes >> 4), d, S::kHalfSlabs - kSlabs);
       commit(smem_u32(&sh.bars.s_full[buf]));
-      if (++st == S::kStages) {
-        st = 0;
-        ++round;
-      }
+      ring.next_half();
+      ring.next_tile();
     }
     commit(smem_u32(&sh.bars.q_empty));
   }
@@ -1014,16 +1213,17 @@ __device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared
 
 // Issues the sums' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& sh, uint32_t sK, uint32_t sP,
-                                           uint32_t tmem) {
+__device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
-  const uint64_t dP = smem_desc(sP, 16, 1024), dV = smem_desc(sK, kSlabBytes, 1024);
-  uint32_t it = 0, st = 0, segs = 0;
+  const uint64_t d_p = smem_desc(smem + S::kPAt, 16, 1024), d_v = smem_desc(smem, kSlabBytes, 1024);
+  uint32_t it = 0, segs = 0;
+  Ring<OP> ring;
   while (true) {
     Segment x;
     const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
     if (tiles == 0) return true;
+    ring.skip_tile();  // the q rows
     if (segs > 0 && !warp_wait(smem_u32(&sh.bars.o_empty), (segs - 1) & 1u, ab)) return false;
     ++segs;
     for (int i = 0; i < tiles; ++i, ++it) {
@@ -1031,13 +1231,15 @@ __device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& 
       if (!warp_wait(smem_u32(&sh.bars.p_full[buf]), (it / 2) & 1u, ab)) return false;
       fence_async();
       fence_after();
-      const uint64_t v = dV + st * (S::kTile >> 4), w = dP + (S::kPBufs > 1 ? buf * (S::kP >> 4) : 0u);
-      if (i == 0) {
-        pv_products<OP, true>(sh, w, v, tmem, st, buf);
-      } else {
-        pv_products<OP, false>(sh, w, v, tmem, st, buf);
+      const uint64_t w = d_p + (S::kPBufs > 1 ? buf * (S::kP >> 4) : 0u);
+#pragma unroll 1
+      for (uint32_t h = 0; h < 2; ++h) {
+        pv_half<OP>(w, d_v + ring.half * (S::kHalf >> 4), tmem + 128u * h, i > 0 ? 1u : 0u);
+        commit(smem_u32(&sh.bars.empty[ring.half]));
+        ring.next_half();
       }
-      if (++st == S::kStages) st = 0;
+      commit(smem_u32(&sh.bars.pv_done[buf]));
+      ring.next_tile();
     }
   }
 }
@@ -1059,19 +1261,21 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
   scale2 = fabsf(scale2);
   volatile uint32_t* ab = &sh.abort_flag;
   Segment seg;
-  uint32_t it = 0, st = 0, round = 0;
+  uint32_t it = 0;
+  Ring<OP> ring;
   bool good = true;
   while (good && next_segment(p, cur, seg)) {
     float m = -INFINITY;  // the reference maximum of the row, in powers of two
     float l = 0.0f;       // this thread's share of the denominator
+    ring.skip_tile();     // the q rows
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
       const uint32_t buf = it & 1u;
       // the flags first: they are there before the scores, and may have come by the copy engine
-      good = warp_wait(smem_u32(&sh.bars.kv_full[st][0]), round & 1u, ab) && good;
+      good = warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab) && good;
       uint32_t ok[kN / 4];
 #pragma unroll
       for (int j = 0; j < kN / 16; ++j) {
-        const uint4 f = ld_shared(smem_u32(&sh.valid[st][part * kN + 16 * j]));
+        const uint4 f = ld_shared(smem_u32(&sh.valid[ring.slot][part * kN + 16 * j]));
         ok[4 * j] = f.x;
         ok[4 * j + 1] = f.y;
         ok[4 * j + 2] = f.z;
@@ -1088,10 +1292,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.s_empty[buf]));
-      if (++st == Shape<OP>::kStages) {
-        st = 0;
-        ++round;
-      }
+      ring.skip_tile();
       if (negative) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) v[j] ^= 0x80000000u;
@@ -1145,17 +1346,17 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
           uint32_t h, x;
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
           // each remainder is exact in fp16: it has the bits the term left over
-          const uint32_t t0 = e5m2x2(h), r0 = sub_f16x2(h, e5m2x2_to_f16x2(t0));
-          const uint32_t t1 = e5m2x2(r0), r1 = sub_f16x2(r0, e5m2x2_to_f16x2(t1));
-          x = e5m2x2(r1);
+          const uint32_t t0 = near_e5m2(h), r0 = sub_f16x2(h, t0);
+          const uint32_t t1 = near_e5m2(r0), r1 = sub_f16x2(r0, t1);
+          x = near_e5m2(r1);
           if ((j & 1) == 0) {
             w[j >> 1] = t0;
             mid[j >> 1] = t1;
             lo[j >> 1] = x;
-          } else {
-            w[j >> 1] |= t0 << 16;
-            mid[j >> 1] |= t1 << 16;
-            lo[j >> 1] |= x << 16;
+          } else {  // the upper bytes of four
+            w[j >> 1] = __byte_perm(w[j >> 1], t0, 0x7531);
+            mid[j >> 1] = __byte_perm(mid[j >> 1], t1, 0x7531);
+            lo[j >> 1] = __byte_perm(lo[j >> 1], x, 0x7531);
           }
         } else {
           w[j] = pack_bf16x2(a, b);
@@ -1306,17 +1507,14 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
 
 template <int FMT, int OP>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap map, const Params p) {
+    attend_kernel(const __grid_constant__ CUtensorMap slab_map, const __grid_constant__ CUtensorMap half_map,
+                  const Params p) {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
-  // a half of a tile: one arrival a loader warp, and one a thread where rows come by asynchronous copies
-  constexpr uint32_t kFill = (R::kDecode ? 1 : 33) * R::kLoad;
   extern __shared__ uint8_t dsmem[];
   __shared__ Shared sh;
   const int warp = uniform(static_cast<int>(threadIdx.x) >> 5);
-  const uint32_t sQ = (smem_u32(dsmem) + 1023u) & ~1023u;
-  const uint32_t sK = sQ + S::kTile;
-  const uint32_t sP = sK + S::kStages * S::kTile;
+  const uint32_t smem = (smem_u32(dsmem) + 1023u) & ~1023u;
   if (warp == R::kScores) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                  "r"(kTmemCols)
@@ -1331,11 +1529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto init = [](uint64_t* b, uint32_t n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < S::kStages; ++i) {
-      for (int h = 0; h < 2; ++h) {
-        init(&sh.bars.kv_full[i][h], kFill);
-        init(&sh.bars.kv_empty[i][h], 1);
-      }
+    for (int i = 0; i < S::kHalves; ++i) {
+      init(&sh.bars.full[i], kArrivals * R::kLoad);
+      init(&sh.bars.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       init(&sh.bars.s_full[i], 1);
@@ -1343,15 +1539,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       init(&sh.bars.p_full[i], R::kSoft);
       init(&sh.bars.pv_done[i], 1);
     }
-    init(&sh.bars.q_full, 32 * R::kLoad);
     init(&sh.bars.q_empty, 1);
     init(&sh.bars.o_empty, R::kSoft);
     init(&sh.bars.drained[0], 1);
     init(&sh.bars.drained[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x == 32 && p.box_rows > 0)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+  if (threadIdx.x == 32 && p.box_rows > 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&slab_map)) : "memory");
+    if (p.box_rows == kKeys) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&half_map)) : "memory");
+  }
   pdl_wait();     // the lengths, q and the cache rows may come from the upstream kernel
   pdl_trigger();  // the joining kernel waits for this grid's end itself
   fence_before();
@@ -1364,15 +1561,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       float scale2 = p.sm_scale * 1.4426950408889634f;  // powers of two: log2(e)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
-      softmax_role<OP, R::kSoft>(p, cur, sh, sP, tmem, scale2);
-    } else if (warp == R::kScores) {
-      if (!issue_scores<OP>(p, cur, sh, sQ, sK, tmem)) give_up(p, &sh.abort_flag);
-      drain(&sh.bars.drained[0], &sh.never);
-    } else if (warp == R::kSums) {
-      if (!issue_sums<OP>(p, cur, sh, sK, sP, tmem)) give_up(p, &sh.abort_flag);
-      drain(&sh.bars.drained[1], &sh.never);
+      softmax_role<OP, R::kSoft>(p, cur, sh, smem + S::kPAt, tmem, scale2);
+    } else if (warp < R::kScores) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kLoadRegs));
+      loader<FMT, OP>(p, Maps{&slab_map, &half_map}, cur, sh, smem);
     } else {
-      loader<FMT, OP>(p, &map, cur, sh, sQ, sK);
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+      if (warp == R::kScores) {
+        if (!issue_scores<OP>(p, cur, sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        drain(&sh.bars.drained[0], &sh.never);
+      } else if (warp == R::kSums) {
+        if (!issue_sums<OP>(p, cur, sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        drain(&sh.bars.drained[1], &sh.never);
+      }
     }
   }
   fence_before();
@@ -1661,8 +1862,8 @@ Kernels kernels_of(int32_t tile_cost) {
                  static_cast<int32_t>(Shape<OP>::kImage), tile_cost, OP == kF8 ? kCostF8 : kCostImage};
 }
 
-const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kernels_of<MLA_CACHE_E4M3, kBf16>(kCostCodes),
-                             kernels_of<MLA_CACHE_MX, kBf16>(kCostCodes), kernels_of<MLA_CACHE_E4M3, kF8>(kCostF8)};
+const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kernels_of<MLA_CACHE_E4M3, kBf16>(kCostE4m3),
+                             kernels_of<MLA_CACHE_MX, kBf16>(kCostMx), kernels_of<MLA_CACHE_E4M3, kF8>(kCostF8)};
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
@@ -1821,7 +2022,7 @@ mla_status mla_prefix_attend_launch(
     g_smem_ready[dev][k].store(true, std::memory_order_release);
   }
   // Tensor copies: rows of 16-bit values or codes as they are, in pages of a multiple of eight rows
-  CUtensorMap map{};
+  CUtensorMap slab_map{}, half_map{};
   p.box_rows = 0;
   const bool decode = k == MLA_CACHE_MX || k == MLA_CACHE_E4M3;
   const int64_t cache_rows = num_blocks * block_size;
@@ -1834,16 +2035,23 @@ mla_status mla_prefix_attend_launch(
     const cuuint64_t strides[1] = {576 * elem};
     const cuuint32_t size[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box)};
     const cuuint32_t step[2] = {1, 1};
-    if (encode(&map, k == 3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-               const_cast<void*>(cache), dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return MLA_ERR_INVALID_ARG;
+    const CUtensorMapDataType type = k == 3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUresult r = encode(&slab_map, type, 2, const_cast<void*>(cache), dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS && box == kKeys) {
+      const cuuint64_t dims3[3] = {size[0], dims[1], kDv / size[0]};  // bytes of a slab, rows, value slabs
+      const cuuint64_t strides3[2] = {strides[0], 128};
+      const cuuint32_t size3[3] = {size[0], kKeys, static_cast<cuuint32_t>(kDv / size[0] / 2)};
+      const cuuint32_t step3[3] = {1, 1, 1};
+      r = encode(&half_map, type, 3, const_cast<void*>(cache), dims3, strides3, size3, step3, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    if (r != CUDA_SUCCESS) return MLA_ERR_INVALID_ARG;
     p.box_rows = box;
     p.image = nullptr;
   }
   void* args[] = {&p};
-  void* attend_args[] = {&map, &p};
+  void* attend_args[] = {&slab_map, &half_map, &p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;
   if (p.image != nullptr) {
     s = launch(ks.image, dim3(static_cast<unsigned>(lay.image_tiles), static_cast<unsigned>(G), 1), 256, 0, pdl, stream,
