@@ -130,10 +130,12 @@ struct Roles {
   static constexpr int kLoad = kDecode ? 8 : 4;
   static constexpr int kScores = 12;          // the warp that issues the scores' products
   static constexpr int kSums = 13;            // and the sums'
+  static constexpr int kFinds = 14;           // and the one that finds the segments
+  static constexpr int kTakers = 14;          // warps that take them up
   static constexpr int kLoadRegs = kDecode ? 152 : 176;     // with kIssueRegs and the softmax's 128: 512 for four times four warps
   static constexpr int kRows = kRowsTile / kLoad;           // rows of a loader warp
 };
-// Sixteen warps (two without work) of 128 registers; the last four hand on to the loaders
+// Sixteen warps (one without work) of 128 registers; the last four hand on to the loaders
 // what issuing products does not need.
 constexpr int kThreads = 32 * 16;
 constexpr int kIssueRegs = 80;
@@ -148,7 +150,7 @@ constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
 // What the deal counts (measured cycles, in hundreds): a key tile, by how it
 // comes, and a segment's start and end.
-constexpr int kCostImage = 23, kCostRows = 25, kCostE4m3 = 66, kCostMx = 80, kCostF8 = 20, kCostSegment = 90;
+constexpr int kCostPrefix = 24, kCostRows = 32, kCostE4m3 = 58, kCostMx = 70, kCostF8 = 20, kCostSegment = 110;
 
 struct Params {
   const uint8_t* q;
@@ -179,7 +181,7 @@ struct Params {
   int32_t ctas;       // CTAs of the attention kernel
   int32_t image_bytes;  // of one tile's image
   int32_t box_rows;     // cache rows of one tensor copy (8, 16, 32 or 64), or 0: none are made
-  int32_t tile_cost, image_cost;  // of a tile read from the cache, from an image
+  int32_t tile_cost, prefix_cost;  // of a tile of own keys, of a prefix
   int32_t* status;
 };
 
@@ -198,6 +200,8 @@ __device__ __forceinline__ void report(int32_t* status, int32_t bit) {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // ---- units ---------------------------------------------------------------------
 
@@ -238,63 +242,80 @@ __device__ __forceinline__ void group_tokens(const Params& p, int64_t g, int64_t
   bad = lo != a || hi != b;
 }
 
+// A token's own keys, given their number.
+__device__ __forceinline__ Unit token_unit(const Params& p, int64_t t, int64_t len, bool& bad) {
+  Unit x;
+  x.rows0 = t * p.H;
+  x.rows = p.H;
+  x.table = p.block_table + t * p.table_stride;
+  x.image = nullptr;
+  x.prefix = false;
+  x.part0 = t * ((p.H + kRowsTile - 1) / kRowsTile);
+  bad = len > p.table_keys;
+  x.len = cut(len, 0, p.table_keys);
+  x.tile_cost = p.tile_cost;
+  return x;
+}
+
 // Unit u: group u for u < G, else token u - G.  `bad`: something had to be cut.
 // Row tiles are numbered from rows0 / 64 + g on for a group: floor(x) + 1 >=
 // ceil(x), so the numbers of consecutive groups do not meet.
 __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
+  if (u >= p.G) return token_unit(p, u - p.G, p.table_keys > 0 ? __ldcg(p.seq_lens + (u - p.G)) : 0, bad);
   Unit x;
-  int64_t len, keys;
-  if (u < p.G) {
-    int64_t lo, hi;
-    group_tokens(p, u, lo, hi, bad);
-    len = __ldcg(p.prefix_lens + u);
-    keys = p.prefix_keys;
-    x.rows0 = lo * p.H;
-    x.rows = (hi - lo) * p.H;
-    x.table = p.prefix_table + u * p.prefix_stride;
-    x.image = p.image != nullptr ? p.image + u * p.image_tiles * p.image_bytes : nullptr;
-    x.prefix = true;
-    x.part0 = x.rows0 / kRowsTile + u;
-  } else {
-    const int64_t t = u - p.G;
-    bad = false;
-    len = p.table_keys > 0 ? __ldcg(p.seq_lens + t) : 0;
-    keys = p.table_keys;
-    x.rows0 = t * p.H;
-    x.rows = p.H;
-    x.table = p.block_table + t * p.table_stride;
-    x.image = nullptr;
-    x.prefix = false;
-    x.part0 = t * ((p.H + kRowsTile - 1) / kRowsTile);
-  }
-  bad = bad || len > keys;
-  x.len = cut(len, 0, keys);
-  x.tile_cost = x.image != nullptr ? p.image_cost : p.tile_cost;
+  int64_t lo, hi;
+  group_tokens(p, u, lo, hi, bad);
+  const int64_t len = __ldcg(p.prefix_lens + u);
+  x.rows0 = lo * p.H;
+  x.rows = (hi - lo) * p.H;
+  x.table = p.prefix_table + u * p.prefix_stride;
+  x.image = p.image != nullptr ? p.image + u * p.image_tiles * p.image_bytes : nullptr;
+  x.prefix = true;
+  x.part0 = x.rows0 / kRowsTile + u;
+  bad = bad || len > p.prefix_keys;
+  x.len = cut(len, 0, p.prefix_keys);
+  x.tile_cost = p.prefix_cost;
   return x;
 }
 
-// One segment: rows [row0, row0 + rows) against key tiles [k0, k1).
+// One segment: rows [row0, row0 + rows) against key tiles [k0, k1) of `len` keys.
 struct Segment {
-  int64_t row0;
-  int32_t rows;
-  int32_t k0, k1;
-  int64_t len;
   const int32_t* table;
   const uint8_t* image;
   uint8_t* part;
+  int32_t row0, rows;
+  int32_t k0, k1;  // equal: there are no more segments
+  int32_t len;
   int32_t part_rows;
 };
 
+// A place in the CTA's run.
 struct Cursor {
   int64_t pos, end;  // this CTA's run
   int64_t base, u;   // where unit u starts
   const Unit* known;  // unit u, if it has been looked up already
+  int64_t window;    // lane i knows the number of keys of token `window` + i
+  int32_t window_len;
 };
 
+// The next segment, by a whole warp.
 __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment& s) {
   while (c.pos < c.end) {
     bool bad;
-    const Unit x = c.known != nullptr ? *c.known : unit_at(p, c.u, bad);
+    Unit x;
+    if (c.known != nullptr) {
+      x = *c.known;
+    } else if (c.u < p.G) {
+      x = unit_at(p, c.u, bad);
+    } else {
+      const int64_t t = c.u - p.G;
+      if (t - c.window >= 32) {
+        const int64_t mine = t + (threadIdx.x & 31u);
+        c.window = t;
+        c.window_len = p.table_keys > 0 && mine < p.T ? __ldcg(p.seq_lens + mine) : 0;
+      }
+      x = token_unit(p, t, __shfl_sync(0xffffffffu, c.window_len, static_cast<int>(t - c.window)), bad);
+    }
     const int64_t per = x.row_cost(), n = x.row_tiles() * per;
     if (c.pos >= c.base + n) {
       c.base += n;
@@ -302,17 +323,17 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
       c.known = nullptr;
       continue;
     }
-    const int64_t off = c.pos - c.base, r = off / per, from = off - r * per;
+    const int64_t off = c.pos - c.base, r = off < per ? 0 : off / per, from = off - r * per;
     const int64_t to = per - from < c.end - c.pos ? per : from + (c.end - c.pos);
     c.pos += to - from;
     // the key tiles that start in this run
     const int64_t k = x.tile_at(from), k_end = to < per ? x.tile_at(to) : x.key_tiles();
     if (k >= k_end) continue;
-    s.row0 = x.rows0 + r * kRowsTile;
+    s.row0 = static_cast<int32_t>(x.rows0 + r * kRowsTile);
     s.rows = static_cast<int32_t>(x.rows - r * kRowsTile < kRowsTile ? x.rows - r * kRowsTile : kRowsTile);
     s.k0 = static_cast<int32_t>(k);
     s.k1 = static_cast<int32_t>(k_end);
-    s.len = x.len;
+    s.len = static_cast<int32_t>(x.len);
     s.table = x.table;
     s.image = x.image;
     s.part_rows = x.prefix ? kRowsTile : p.own_rows;
@@ -422,7 +443,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   __syncwarp();
 }
 
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -590,22 +610,21 @@ __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// Segments known ahead: more than the roles are ever apart would be of no use.
+constexpr uint32_t kSegments = 8;
+
 struct Bars {
   uint64_t full[kMaxHalves], empty[kMaxHalves];
   uint64_t q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2], o_empty;  // [tile & 1]
   uint64_t drained[2];
-};
-
-struct SegmentInfo {
-  const uint8_t* image;
-  int32_t row0, rows;  // q rows
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
 };
 
 struct Shared {
   Bars bars;
-  SegmentInfo segments[8];
+  Segment segments[kSegments];
   uint32_t tmem;
   uint32_t abort_flag;
   uint32_t never;  // stays 0
@@ -633,28 +652,42 @@ __device__ __forceinline__ const uint8_t* row_at(const uint8_t* mine, int i) {
   return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i));
 }
 
-// Half h of ROWS rows that need no decoding, piece by piece: f(slab, row, piece,
-// address of the piece or null).
-template <int OP, int ROWS, class F>
-__device__ __forceinline__ void each_piece(const uint8_t* mine, int h, int lane, const F& f) {
-  constexpr int kPieces = 8 * Shape<OP>::kHalfSlabs;   // of a row's half: 32 or 16
-  constexpr int kAtOnce = 32 / kPieces;                // rows a warp covers at once
+// ROWS rows that need no decoding, as a lane copies them, 16 bytes at a time: of
+// step i it copies one piece of row `of`.  (All rows' addresses are had before the
+// first copy: a shuffle between two copies waits for the first.)
+template <int OP, int ROWS>
+struct Pieces {
+  static constexpr int kHalf = 8 * Shape<OP>::kHalfSlabs;  // pieces of a row's half: 32 or 16
+  static constexpr int kAtOnce = 32 / kHalf;               // rows a warp covers at once
+  static constexpr int kPe = 4 * Shape<OP>::kElem;         // pieces of the rotary values: 8 or 4
+  const uint8_t* of[ROWS / kAtOnce];
+  const uint8_t* of_pe[ROWS * kPe / 32];
+
+  __device__ __forceinline__ Pieces(const uint8_t* mine, int lane) {
 #pragma unroll
-  for (int i = 0; i < ROWS / kAtOnce; ++i) {
-    const int r = kAtOnce * i + lane / kPieces, c = lane % kPieces;
-    const uint8_t* src = row_at(mine, r);
-    f(Shape<OP>::kHalfSlabs * h + (c >> 3), r, c & 7, src != nullptr ? src + 16 * (kPieces * h + c) : nullptr);
+    for (int i = 0; i < ROWS / kAtOnce; ++i) of[i] = row_at(mine, kAtOnce * i + lane / kHalf);
+#pragma unroll
+    for (int i = 0; i < ROWS * kPe / 32; ++i) of_pe[i] = row_at(mine, (32 / kPe) * i + lane / kPe);
   }
-  if (h == 0) {
-    constexpr int kPe = 4 * Shape<OP>::kElem;          // pieces of the rotary values: 8 or 4
+  // Half h's values, or the rotary values, piece by piece: f(slab, row, piece, address of the piece or null).
+  template <class F>
+  __device__ __forceinline__ void values(int h, int lane, const F& f) const {
 #pragma unroll
-    for (int i = 0; i < ROWS * kPe / 32; ++i) {
-      const int r = (32 / kPe) * i + lane / kPe, c = lane % kPe;
-      const uint8_t* src = row_at(mine, r);
-      f(Shape<OP>::kPeSlab, r, c, src != nullptr ? src + 16 * (2 * kPieces + c) : nullptr);
+    for (int i = 0; i < ROWS / kAtOnce; ++i) {
+      const int c = lane % kHalf;
+      f(Shape<OP>::kHalfSlabs * h + (c >> 3), kAtOnce * i + lane / kHalf, c & 7,
+        of[i] != nullptr ? of[i] + 16 * (kHalf * h + c) : nullptr);
     }
   }
-}
+  template <class F>
+  __device__ __forceinline__ void rotary(int lane, const F& f) const {
+#pragma unroll
+    for (int i = 0; i < ROWS * kPe / 32; ++i) {
+      const int c = lane % kPe;
+      f(Shape<OP>::kPeSlab, (32 / kPe) * i + lane / kPe, c, of_pe[i] != nullptr ? of_pe[i] + 16 * (2 * kHalf + c) : nullptr);
+    }
+  }
+};
 
 // What a lane holds of its warp's eight quantised rows.  Half h of rows 2 j and
 // 2 j + 1 (lanes 0..15 and 16..31): codes[4 h + j], 16 codes a lane.  The rest
@@ -748,49 +781,74 @@ __device__ __forceinline__ void store_half(const Raw<FMT>& raw, int h, int row0,
 
 // ---- the roles ---------------------------------------------------------------------
 
+// On a wait that ran out (not on another role's): says so, and that all roles stop.
+__device__ __forceinline__ void give_up(const Params& p, uint32_t* abort_flag) {
+  volatile uint32_t* ab = abort_flag;
+  if ((threadIdx.x & 31u) == 0u && *ab == 0u) {
+    *ab = 1u;
+    report(p.status, MLA_STATUS_TIMEOUT);
+  }
+}
+
+// One warp finds the CTA's segments for all the others.  Found by each of them
+// for itself, a segment cost every role some 2000 cycles (lengths to be fetched,
+// 64-bit divisions), one role behind the other.
+__device__ __forceinline__ bool find_segments(const Params& p, Cursor cur, Shared& sh) {
+  for (uint32_t n = 0;; ++n) {
+    Segment s;
+    if (!next_segment(p, cur, s)) s.k0 = s.k1 = 0;
+    if (n >= kSegments &&
+        !warp_wait(smem_u32(&sh.bars.seg_empty[n % kSegments]), (n / kSegments - 1) & 1u, &sh.abort_flag))
+      return false;
+    if ((threadIdx.x & 31u) == 0u) {
+      sh.segments[n % kSegments] = s;
+      arrive(smem_u32(&sh.bars.seg_full[n % kSegments]));
+    }
+    __syncwarp();
+    if (s.k0 == s.k1) return true;
+  }
+}
+
+// Segment n, when it is known; and the warp's leave of it.
+__device__ __forceinline__ bool segment_known(Shared& sh, uint32_t n) {
+  return warp_wait(smem_u32(&sh.bars.seg_full[n % kSegments]), (n / kSegments) & 1u, &sh.abort_flag);
+}
+__device__ __forceinline__ void segment_done(Shared& sh, uint32_t n) {
+  __syncwarp();
+  if ((threadIdx.x & 31u) == 0u) arrive(smem_u32(&sh.bars.seg_empty[n % kSegments]));
+}
+
 // A walk over this CTA's key tiles, one at a time.  A tile that comes by copies of
 // many bytes each (an image's, or a whole one by tensor copies) is one loader
 // warp's work, in turn; of the others each warp has some rows.
 struct TileWalk {
-  Cursor cur;
-  const int32_t* table;
-  int32_t len, kt, k0, k1;
-  int32_t seg;     // segments begun
-  int32_t owned;   // tiles of the segment before this one are one warp's each
-  bool copied;     // the segment's tiles come from an image
-  bool any;        // not yet behind the last
+  const int32_t* table = nullptr;
+  int32_t len = 0, kt = 0, k0 = 0, k1 = 0;
+  uint32_t seg = 0;    // segments begun
+  int32_t owned = 0;   // tiles of the segment before this one are one warp's each
+  bool copied = false;  // the segment's tiles come from an image
+  bool any = true;     // not yet behind the last
 
-  __device__ __forceinline__ void start(const Cursor& c) {
-    cur = c;
-    kt = k0 = k1 = seg = len = owned = 0;
-    table = nullptr;
-    copied = false;
-    any = true;
-  }
-  // To the next tile.  `boxes`: tensor copies are made.
-  __device__ __forceinline__ void next(const Params& p, Shared& sh, bool boxes) {
-    if (!any || ++kt < k1) return;
-    Segment s;
-    any = uniform(next_segment(p, cur, s) ? 1 : 0) != 0;
-    if (!any) return;
+  // To the next tile; false: a wait ran out.  `boxes`: tensor copies are made.
+  __device__ __forceinline__ bool next(Shared& sh, bool boxes) {
+    if (!any || ++kt < k1) return true;
+    if (!segment_known(sh, seg)) return false;
+    const Segment& s = sh.segments[seg % kSegments];
+    kt = k0 = uniform(s.k0);
+    k1 = uniform(s.k1);
+    any = k0 < k1;
     table = s.table;
-    len = static_cast<int32_t>(s.len);
-    kt = k0 = s.k0;
-    k1 = s.k1;
-    copied = s.image != nullptr;
+    len = uniform(s.len);
+    copied = uniform(s.image != nullptr ? 1 : 0) != 0;
     owned = copied ? k1 : boxes ? len / kKeys : 0;
     ++seg;
-    // Kept for the tiles' own turn.  Every loader warp writes the same values;
-    // they are at most 2 + 2 + 1 segments apart, so none is overwritten too early.
-    volatile SegmentInfo& i = sh.segments[seg & 7];
-    i.image = s.image;
-    i.row0 = static_cast<int32_t>(s.row0);
-    i.rows = s.rows;
+    return true;
   }
 };
 
 struct Tile {
-  int32_t kt, seg;
+  int32_t kt;
+  uint32_t seg;
   bool copied, first, any;
   bool whole;  // one warp's work
   bool mine;   // this warp has work with it
@@ -839,16 +897,18 @@ __device__ __forceinline__ const uint8_t* q_row(const Params& p, int32_t row0, i
 }
 
 // A loader warp's part of the segment's 64 q rows, to `to(slab, row, piece)`; the
-// two halves' barriers get the warp's arrivals.
-template <int FMT, int OP, class To>
-__device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t rows, const To& to, uint32_t full0,
-                                       uint32_t full1, int warp, int lane) {
+// two halves' barriers get the warp's arrivals.  What stays in shared memory is
+// written once `free()` has waited for the previous segment's scores.
+template <int FMT, int OP, class To, class Free>
+__device__ __forceinline__ bool load_q(const Params& p, int32_t row0, int32_t rows, const To& to, const Free& free,
+                                       uint32_t full0, uint32_t full1, int warp, int lane) {
   constexpr int kRows = Roles<FMT, OP>::kRows;
+  constexpr bool kStay = Shape<OP>::kQSlabs > 0;
   bool ok;
   const uint8_t* mine = q_row(p, row0, rows, kRows * warp + lane % kRows, ok);
   if (!ok || lane >= kRows) mine = nullptr;
-  uint32_t arrivals = 1;
   if (OP == kBf16 && p.q_fp8) {
+    if (!free()) return false;
 #pragma unroll
     for (int i = 0; i < kRows / 8; ++i) {
       const uint8_t* eight = row_at(mine, 8 * i + (lane & 7));
@@ -858,22 +918,27 @@ __device__ __forceinline__ void load_q(const Params& p, int32_t row0, int32_t ro
       store_half<MLA_CACHE_E4M3>(raw, 0, kRows * warp + 8 * i, lane, put);
       store_half<MLA_CACHE_E4M3>(raw, 1, kRows * warp + 8 * i, lane, put);
     }
-    fence_async();
-    arrivals = kArrivals;
+    __syncwarp();
+    if (lane == 0) {
+      arrive(full0, kArrivals);
+      arrive(full1, kArrivals);
+    }
   } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      each_piece<OP, kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
-        cp_async16(to(s, kRows * warp + r, c), src != nullptr ? src : p.q, src != nullptr);
-      });
+    const Pieces<OP, kRows> pieces(mine, lane);
+    auto copy = [&](int s, int r, int c, const uint8_t* src) {
+      cp_async16(to(s, kRows * warp + r, c), src != nullptr ? src : p.q, src != nullptr);
+    };
+    pieces.values(0, lane, copy);
+    if (!kStay) pieces.rotary(lane, copy);
     cp_async_arrive(full0);
+    if (lane == 0) arrive(full0);
+    if (kStay && !free()) return false;
+    pieces.values(1, lane, copy);
+    if (kStay) pieces.rotary(lane, copy);
     cp_async_arrive(full1);
+    if (lane == 0) arrive(full1);
   }
-  __syncwarp();
-  if (lane == 0) {
-    arrive(full0, arrivals);
-    arrive(full1, arrivals);
-  }
+  return true;
 }
 
 // The cache as seen by tensor copies: 128 bytes of box_rows rows; and where that is
@@ -886,8 +951,8 @@ struct Maps {
 // half's barrier counts kArrivals of each warp: one of its own, and one of each
 // thread's asynchronous copies where there are any.
 template <int FMT, int OP>
-__device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, const Cursor& cur, Shared& sh,
-                                           uint32_t smem, bool& bad_page) {
+__device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Shared& sh, uint32_t smem,
+                                           bool& bad_page) {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
   constexpr bool kDecode = R::kDecode;
@@ -904,10 +969,8 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
   Ring<OP> ring;
   // the ring's next half, when it is free
   auto acquire = [&]() { return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, ab); };
-  auto fill_q = [&](int seg) {
-    const volatile SegmentInfo& info = sh.segments[seg & 7];
-    // the previous segment's scores have been computed
-    if (seg > 1 && !warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab)) return false;
+  auto fill_q = [&](uint32_t seg) {
+    const Segment& info = sh.segments[(seg - 1) % kSegments];
     const uint32_t full0 = smem_u32(&sh.bars.full[ring.half]), base0 = smem + ring.half * S::kHalf;
     if (!acquire()) return false;
     ring.next_half();
@@ -922,11 +985,10 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
              : s >= S::kHalfSlabs ? piece_addr(base1, s - S::kHalfSlabs, r, c)
                                   : piece_addr(base0, s, r, c);
     };
-    load_q<FMT, OP>(p, info.row0, info.rows, to, full0, full1, warp, lane);
-    return true;
+    auto free = [&]() { return seg <= 1 || warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab); };
+    return load_q<FMT, OP>(p, info.row0, info.rows, to, free, full0, full1, warp, lane);
   };
-  w.start(cur);
-  w.next(p, sh, boxes > 0);
+  if (!w.next(sh, boxes > 0)) return false;
   Tile now(w, warp, R::kLoad);
   auto fetch = [&](const Tile& t) {
     if (!t.any || !t.mine || t.copied) return;
@@ -949,13 +1011,13 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
   if constexpr (kDecode) {
     if (!now.copied) load_rows<FMT>(raw, mine, lane);
   }
-  w.next(p, sh, boxes > 0);
+  if (!w.next(sh, boxes > 0)) return false;
   Tile then(w, warp, R::kLoad);
   fetch(then);
   while (now.any) {
     if (now.first && now.seg > 1 && !fill_q(now.seg)) return false;
     locate(then, mine_next, box_next);
-    w.next(p, sh, boxes > 0);
+    if (!w.next(sh, boxes > 0)) return false;
     const Tile after(w, warp, R::kLoad);
     fetch(after);
     if (!now.mine) {
@@ -980,17 +1042,19 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
           if constexpr (kDecode) {
             store_half<FMT>(raw, h, row0, lane, [&](int s, int r, int c, const uint4& v) { st_shared(to(s, r, c), v); });
           } else {
-            each_piece<OP, R::kRows>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
+            const Pieces<OP, R::kRows> pieces(mine, lane);
+            auto copy = [&](int s, int r, int c, const uint8_t* src) {
               cp_async16(to(s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
-            });
+            };
+            pieces.values(h, lane, copy);
+            if (h == 0) pieces.rotary(lane, copy);
             cp_async_arrive(full);
           }
           __syncwarp();
           if (lane == 0) arrive(full, kDecode ? kArrivals : 1);
         } else if (now.copied) {
           if (elect_one()) {
-            const volatile SegmentInfo& info = sh.segments[now.seg & 7];
-            const uint8_t* image = info.image + static_cast<int64_t>(now.kt) * S::kImage;
+            const uint8_t* image = sh.segments[(now.seg - 1) % kSegments].image + static_cast<int64_t>(now.kt) * S::kImage;
             arrive(full, kArrivals * R::kLoad - 1);
             arrive_expect(full, S::kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
             bulk_copy(base, image + h * S::kHalf, S::kHalf, full);
@@ -1005,9 +1069,11 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
           const uint32_t gone = __ballot_sync(0xffffffffu, lane < boxes && mine == nullptr);
           const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
           const int slabs = S::kHalfSlabs + (h == 0 ? 1 : 0);
-          if (h == 0)
-            for (int i = lane; i < kKeys; i += 32) valid[i] = (gone >> (i / p.box_rows)) & 1u ? 0 : 1;
+          if (h == 0 && lane < kKeys / 4) reinterpret_cast<uint32_t*>(valid)[lane] = 0x01010101u;
           if (gone != 0u) {
+            __syncwarp();
+            if (h == 0 && lane < boxes && mine == nullptr)
+              for (int i = 0; i < p.box_rows; ++i) valid[lane * p.box_rows + i] = 0;
             for (int i = lane; i < slabs * kKeys * 8; i += 32) {
               const int s = i / (kKeys * 8), r = (i >> 3) % kKeys;
               if ((gone >> (r / p.box_rows)) & 1u)
@@ -1041,6 +1107,7 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
     }
     // Behind the tile's last arrival: an arrival waits for the loads before it.
     if constexpr (kDecode) load_rows<FMT>(raw, mine_next, lane);
+    if (!then.any || then.first) segment_done(sh, now.seg - 1);
     now = then;
     then = after;
     mine = mine_next;
@@ -1050,10 +1117,9 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, co
 }
 
 template <int FMT, int OP>
-__device__ __forceinline__ void loader(const Params& p, const Maps& maps, const Cursor& cur, Shared& sh,
-                                       uint32_t smem) {
+__device__ __forceinline__ void loader(const Params& p, const Maps& maps, Shared& sh, uint32_t smem) {
   bool bad_page = false;
-  const bool good = load_tiles<FMT, OP>(p, maps, cur, sh, smem, bad_page);
+  const bool good = load_tiles<FMT, OP>(p, maps, sh, smem, bad_page);
   // no copy may be under way when the CTA ends: on the way out after a timeout
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1061,10 +1127,7 @@ __device__ __forceinline__ void loader(const Params& p, const Maps& maps, const 
     for (int i = 0; i < Shape<OP>::kHalves; ++i)
       for (uint32_t parity = 0; parity < 2; ++parity) (void)warp_wait(smem_u32(&sh.bars.full[i]), parity, &sh.never);
   }
-  if (!good && (threadIdx.x & 31u) == 0u && *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) == 0u) {
-    *reinterpret_cast<volatile uint32_t*>(&sh.abort_flag) = 1u;
-    report(p.status, MLA_STATUS_TIMEOUT);
-  }
+  if (!good) give_up(p, &sh.abort_flag);
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
 }
 
@@ -1144,24 +1207,15 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t* never) {
   (void)warp_wait(smem_u32(bar), 0u, never);
 }
 
-// On a wait that ran out (not on another role's): says so, and that all roles stop.
-__device__ __forceinline__ void give_up(const Params& p, uint32_t* abort_flag) {
-  volatile uint32_t* ab = abort_flag;
-  if ((threadIdx.x & 31u) == 0u && *ab == 0u) {
-    *ab = 1u;
-    report(p.status, MLA_STATUS_TIMEOUT);
-  }
-}
-
 // Issues the copies of every segment's q rows to TMEM and the scores' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared& sh, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t d_half = smem_desc(smem, 16, 1024), d_pe = smem_desc(smem + S::kPeAt, 16, 1024);
   const uint64_t d_q = smem_desc(smem + S::kQAt, 16, 1024);  // the q rows' slabs from kQSlab0 on
   const uint32_t q = tmem + kTmemQ;
-  uint32_t it = 0;
+  uint32_t it = 0, segs = 0;
   Ring<OP> ring;
   // The half has come, and the tensor cores may read it.  (The fence between plain
   // stores or asynchronous copies and the tensor cores' reads is made here: made by
@@ -1173,12 +1227,16 @@ __device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared
     return true;
   };
   while (true) {
-    Segment x;
-    const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
+    if (!segment_known(sh, segs)) return false;
+    const Segment& x = sh.segments[segs % kSegments];
+    const int tiles = uniform(x.k1 - x.k0);
     if (tiles == 0) return true;
-    // The products that read the previous segment's q rows have completed: the
-    // loaders waited for that.  Those that read these run behind the copies.
+    segment_done(sh, segs);
     if (!come()) return false;
+    // The products that read the previous segment's q rows have completed.  Those
+    // that read these run behind the copies.
+    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.q_empty), (segs - 1) & 1u, ab)) return false;
+    ++segs;
     q_copy<0, 4 * S::kHalfSlabs>(smem_desc(smem + ring.half * S::kHalf, 16, 1024), tmem);
     if (S::kPeSlab < S::kQSlab0)
       q_copy<4 * S::kPeSlab, S::kPeSteps>(smem_desc(smem + S::kPeAt + ring.slot * kSlabBytes, 16, 1024), tmem);
@@ -1213,23 +1271,25 @@ __device__ __forceinline__ bool issue_scores(const Params& p, Cursor cur, Shared
 
 // Issues the sums' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& sh, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ bool issue_sums(Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t d_p = smem_desc(smem + S::kPAt, 16, 1024), d_v = smem_desc(smem, kSlabBytes, 1024);
   uint32_t it = 0, segs = 0;
   Ring<OP> ring;
   while (true) {
-    Segment x;
-    const int tiles = uniform(next_segment(p, cur, x) ? x.k1 - x.k0 : 0);
+    if (!segment_known(sh, segs)) return false;
+    const Segment& x = sh.segments[segs % kSegments];
+    const int tiles = uniform(x.k1 - x.k0);
     if (tiles == 0) return true;
+    segment_done(sh, segs);
     ring.skip_tile();  // the q rows
     if (segs > 0 && !warp_wait(smem_u32(&sh.bars.o_empty), (segs - 1) & 1u, ab)) return false;
     ++segs;
     for (int i = 0; i < tiles; ++i, ++it) {
       const uint32_t buf = it & 1u;
       if (!warp_wait(smem_u32(&sh.bars.p_full[buf]), (it / 2) & 1u, ab)) return false;
-      fence_async();
+      fence_async();  // the weights came by plain stores (and the rows may have)
       fence_after();
       const uint64_t w = d_p + (S::kPBufs > 1 ? buf * (S::kP >> 4) : 0u);
 #pragma unroll 1
@@ -1248,7 +1308,7 @@ __device__ __forceinline__ bool issue_sums(const Params& p, Cursor cur, Shared& 
 // scores half `half` of the keys, of that (8 warps) half `sub`; of the sums the
 // same half of each 256 columns and half `sub` of the TMEM columns.
 template <int OP, int WARPS>
-__device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared& sh, uint32_t sP, uint32_t tmem,
+__device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32_t sP, uint32_t tmem,
                                              float scale2) {
   constexpr int kN = 32 * 4 / WARPS;           // keys of a thread: 32 or 16
   constexpr int kParts = WARPS / 2;            // threads to a row
@@ -1256,15 +1316,25 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
   const int r = (warp & 1) * 32 + lane;
   const int half = (warp >> 1) & 1, sub = warp >> 2;
   const int part = half * (kParts / 2) + sub;  // keys part * kN ..
+  // the warps that share rows with this one: their barriers, their threads
+  const int bar_a = 1 + 2 * (warp & 1), bar_b = bar_a + 1;
+  constexpr int kShare = 16 * WARPS;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
   const bool negative = scale2 < 0.0f;  // then the scores change sign, and the scale
   scale2 = fabsf(scale2);
   volatile uint32_t* ab = &sh.abort_flag;
-  Segment seg;
   uint32_t it = 0;
   Ring<OP> ring;
   bool good = true;
-  while (good && next_segment(p, cur, seg)) {
+  for (uint32_t segs = 0; good; ++segs) {
+    good = segment_known(sh, segs);
+    if (bar_or(bar_a, kShare, !good)) {  // the warps that share rows leave together
+      good = false;
+      break;
+    }
+    const Segment seg = sh.segments[segs % kSegments];
+    if (seg.k0 == seg.k1) break;
+    segment_done(sh, segs);
     float m = -INFINITY;  // the reference maximum of the row, in powers of two
     float l = 0.0f;       // this thread's share of the denominator
     ring.skip_tile();     // the q rows
@@ -1314,15 +1384,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       const bool first = kt == seg.k0;
       // One vote a tile: whether a row's reference must move, or a wait ran out
       // (then all the warps leave together).
-      const bool moved = bar_or(1, 32 * WARPS, first || top > m + kRescale || !good);
+      const bool moved = bar_or(bar_a, kShare, first || top > m + kRescale || !good);
       float factor = 1.0f;
       if (moved) {
-        if (bar_or(2, 32 * WARPS, !good)) {
+        if (bar_or(bar_b, kShare, !good)) {
           good = false;
           break;
         }
         sh.xch[part][r] = top;
-        bar_sync(2, 32 * WARPS);
+        bar_sync(bar_b, kShare);
         float next = m;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) next = fmaxf(next, sh.xch[i][r]);
@@ -1395,7 +1465,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
         for (int j = 0; j < kN / 8; ++j)
           st_shared(piece_addr(dst, 0, r, part * (kN / 8) + j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
       }
-      fence_async();
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.p_full[buf]));
@@ -1403,7 +1472,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     if (!good) break;
     // ---- the segment's result
     good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab);
-    if (bar_or(1, 32 * WARPS, !good)) {
+    if (bar_or(bar_a, kShare, !good)) {
       good = false;
       break;
     }
@@ -1428,7 +1497,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
     __syncwarp();
     if (lane == 0) arrive(smem_u32(&sh.bars.o_empty));
     sh.xch[part][r] = l;
-    bar_sync(2, 32 * WARPS);
+    bar_sync(bar_b, kShare);
     if (part == 0 && keep) {
       float* stat = reinterpret_cast<float*>(seg.part + static_cast<int64_t>(seg.part_rows) * kChunks * 16);
       float den = l;
@@ -1437,7 +1506,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Cursor cur, Shared
       __stcg(stat + r, OP == kF8 ? (m == -INFINITY ? m : m - kF8Lift) : m);
       __stcg(stat + seg.part_rows + r, den);
     }
-    bar_sync(2, 32 * WARPS);
+    bar_sync(bar_b, kShare);
   }
   if (!good && *ab == 0u && lane == 0) {
     *ab = 1u;
@@ -1477,7 +1546,7 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
     total += sh.warp_sum[w];
   }
   // at least a tile's cost, so that every CTA between a row tile's first and last has one of its key tiles
-  const int64_t least = p.tile_cost > p.image_cost ? p.tile_cost : p.image_cost;
+  const int64_t least = p.tile_cost > p.prefix_cost ? p.tile_cost : p.prefix_cost;
   const int64_t each = (total + p.ctas - 1) / p.ctas > least ? (total + p.ctas - 1) / p.ctas : least;
   Cursor c;
   c.pos = each * blockIdx.x;
@@ -1502,6 +1571,8 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   c.u = sh.first_unit;
   c.base = sh.first_base;
   c.known = &sh.unit;
+  c.window = -64;  // none
+  c.window_len = 0;
   return c;
 }
 
@@ -1541,6 +1612,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     init(&sh.bars.q_empty, 1);
     init(&sh.bars.o_empty, R::kSoft);
+    for (uint32_t i = 0; i < kSegments; ++i) {
+      init(&sh.bars.seg_full[i], 1);
+      init(&sh.bars.seg_empty[i], R::kTakers);
+    }
     init(&sh.bars.drained[0], 1);
     init(&sh.bars.drained[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1561,18 +1636,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       float scale2 = p.sm_scale * 1.4426950408889634f;  // powers of two: log2(e)
       if (p.q_fp8) scale2 *= __ldcg(p.q_scale);
       if (FMT == MLA_CACHE_E4M3) scale2 *= __ldcg(p.kv_scale);
-      softmax_role<OP, R::kSoft>(p, cur, sh, smem + S::kPAt, tmem, scale2);
+      softmax_role<OP, R::kSoft>(p, sh, smem + S::kPAt, tmem, scale2);
     } else if (warp < R::kScores) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kLoadRegs));
-      loader<FMT, OP>(p, Maps{&slab_map, &half_map}, cur, sh, smem);
+      loader<FMT, OP>(p, Maps{&slab_map, &half_map}, sh, smem);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
       if (warp == R::kScores) {
-        if (!issue_scores<OP>(p, cur, sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        if (!issue_scores<OP>(sh, smem, tmem)) give_up(p, &sh.abort_flag);
         drain(&sh.bars.drained[0], &sh.never);
       } else if (warp == R::kSums) {
-        if (!issue_sums<OP>(p, cur, sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        if (!issue_sums<OP>(sh, smem, tmem)) give_up(p, &sh.abort_flag);
         drain(&sh.bars.drained[1], &sh.never);
+      } else if (warp == R::kFinds) {
+        if (!find_segments(p, cur, sh)) give_up(p, &sh.abort_flag);
       }
     }
   }
@@ -1615,11 +1692,13 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
       store_half<FMT>(raw, 0, row0, lane, put);
       store_half<FMT>(raw, 1, row0, lane, put);
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        each_piece<OP, 8>(mine, h, lane, [&](int s, int r, int c, const uint8_t* src) {
-          put(s, row0 + r, c, src != nullptr ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0));
-        });
+      const Pieces<OP, 8> pieces(mine, lane);
+      auto copy = [&](int s, int r, int c, const uint8_t* src) {
+        put(s, row0 + r, c, src != nullptr ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0));
+      };
+      pieces.values(0, lane, copy);
+      pieces.values(1, lane, copy);
+      pieces.rotary(lane, copy);
     }
     if (lane < 8) dst[Shape<OP>::kTile + row0 + lane] = mine != nullptr ? 1 : 0;
     if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
@@ -1852,14 +1931,14 @@ struct Kernels {
   const void* attend;
   const void* image;
   uint32_t smem;
-  int32_t image_bytes, tile_cost, image_cost;
+  int32_t image_bytes, tile_cost, prefix_cost;
 };
 
 template <int FMT, int OP>
 Kernels kernels_of(int32_t tile_cost) {
   return Kernels{reinterpret_cast<const void*>(&attend_kernel<FMT, OP>),
                  reinterpret_cast<const void*>(&image_kernel<FMT, OP>), Shape<OP>::kSmem,
-                 static_cast<int32_t>(Shape<OP>::kImage), tile_cost, OP == kF8 ? kCostF8 : kCostImage};
+                 static_cast<int32_t>(Shape<OP>::kImage), tile_cost, OP == kF8 ? kCostF8 : kCostPrefix};
 }
 
 const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kernels_of<MLA_CACHE_E4M3, kBf16>(kCostE4m3),
@@ -2013,7 +2092,6 @@ mla_status mla_prefix_attend_launch(
   const Kernels& ks = kKernels[k];
   p.image_bytes = ks.image_bytes;
   p.tile_cost = ks.tile_cost;
-  p.image_cost = ks.image_cost;
   if (!g_smem_ready[dev][k].load(std::memory_order_acquire)) {
     // idempotent: two threads racing here both set the same attribute
     const cudaError_t e =
@@ -2050,6 +2128,7 @@ mla_status mla_prefix_attend_launch(
     p.box_rows = box;
     p.image = nullptr;
   }
+  p.prefix_cost = decode && p.image == nullptr ? ks.tile_cost : ks.prefix_cost;
   void* args[] = {&p};
   void* attend_args[] = {&slab_map, &half_map, &p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;
