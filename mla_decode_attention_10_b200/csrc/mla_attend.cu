@@ -148,9 +148,9 @@ constexpr uint32_t kWaitSpins = 1u << 22;
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
-// What the deal counts (measured cycles, in hundreds): a key tile, by how it
-// comes, and a segment's start and end.
-constexpr int kCostPrefix = 24, kCostRows = 32, kCostE4m3 = 58, kCostMx = 70, kCostF8 = 20, kCostSegment = 110;
+// What the deal counts (measured cycles, in hundreds): a key tile, by how it comes,
+// and a segment's start and end, by its rows (their sums are written out).
+constexpr int kCostPrefix = 21, kCostRows = 27, kCostE4m3 = 56, kCostMx = 63, kCostF8 = 18, kCostSegment = 25, kCostRow = 1;
 
 struct Params {
   const uint8_t* q;
@@ -216,12 +216,12 @@ struct Unit {
 
   __device__ __forceinline__ int64_t row_tiles() const { return (rows + kRowsTile - 1) / kRowsTile; }
   __device__ __forceinline__ int64_t key_tiles() const { return (len + kKeys - 1) / kKeys; }
-  int32_t tile_cost;
+  int32_t tile_cost, start_cost;
   // what one row tile counts for in the deal: its start, then its key tiles
-  __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() * tile_cost + kCostSegment : 0; }
+  __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() * tile_cost + start_cost : 0; }
   // the first key tile that starts at or behind position x of the row tile
   __device__ __forceinline__ int64_t tile_at(int64_t x) const {
-    return x > kCostSegment ? (x - kCostSegment + tile_cost - 1) / tile_cost : 0;
+    return x > start_cost ? (x - start_cost + tile_cost - 1) / tile_cost : 0;
   }
   __device__ __forceinline__ int64_t cost() const { return row_tiles() * row_cost(); }
 };
@@ -254,6 +254,7 @@ __device__ __forceinline__ Unit token_unit(const Params& p, int64_t t, int64_t l
   bad = len > p.table_keys;
   x.len = cut(len, 0, p.table_keys);
   x.tile_cost = p.tile_cost;
+  x.start_cost = kCostSegment + kCostRow * p.own_rows;
   return x;
 }
 
@@ -275,6 +276,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, int64_t u, bool& bad) {
   bad = bad || len > p.prefix_keys;
   x.len = cut(len, 0, p.prefix_keys);
   x.tile_cost = p.prefix_cost;
+  x.start_cost = kCostSegment + kCostRow * kRowsTile;
   return x;
 }
 
@@ -996,30 +998,25 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Sh
     at.fetch(p, w.table, w.len, t.kt, look, look >= 0);
   };
   // where the tile's rows lie that this lane looks after
-  const uint8_t *mine = nullptr, *mine_next = nullptr;
-  int32_t box = 0, box_next = 0;
-  auto locate = [&](const Tile& t, const uint8_t*& row, int32_t& first) {
-    row = nullptr;
-    if (!t.any || !t.mine || t.copied) return;
-    row = at.address(p, row_bytes(FMT), bad_page);
-    first = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
+  const uint8_t* mine = nullptr;
+  int32_t box = 0;
+  auto locate = [&](const Tile& t) {
+    mine = nullptr;
+    if (t.any && t.mine && !t.copied) {
+      mine = at.address(p, row_bytes(FMT), bad_page);
+      box = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
+    }
+    if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
   };
   fetch(now);
   // the first segment's q rows go out while page numbers are under way
   if (now.any && !fill_q(now.seg)) return false;
-  locate(now, mine, box);
-  if constexpr (kDecode) {
-    if (!now.copied) load_rows<FMT>(raw, mine, lane);
-  }
+  locate(now);
   if (!w.next(sh, boxes > 0)) return false;
   Tile then(w, warp, R::kLoad);
   fetch(then);
   while (now.any) {
     if (now.first && now.seg > 1 && !fill_q(now.seg)) return false;
-    locate(then, mine_next, box_next);
-    if (!w.next(sh, boxes > 0)) return false;
-    const Tile after(w, warp, R::kLoad);
-    fetch(after);
     if (!now.mine) {
       // waits all the same: a wait tells a phase from the one before, not from the one before that
       ring.next_half();
@@ -1105,13 +1102,14 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Sh
       }
       ring.next_tile();
     }
-    // Behind the tile's last arrival: an arrival waits for the loads before it.
-    if constexpr (kDecode) load_rows<FMT>(raw, mine_next, lane);
+    // (the next tile's rows, if they are decoded, behind this one's last arrival: an
+    // arrival waits for the loads before it)
+    locate(then);
     if (!then.any || then.first) segment_done(sh, now.seg - 1);
     now = then;
-    then = after;
-    mine = mine_next;
-    box = box_next;
+    if (!w.next(sh, boxes > 0)) return false;
+    then = Tile(w, warp, R::kLoad);
+    fetch(then);
   }
   return true;
 }
@@ -1717,8 +1715,14 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
 
 constexpr int kJoinRows = 16, kJoinWorkers = 16, kJoinThreads = kJoinRows * kJoinWorkers;
 
+// a / b; 64-bit divisions are slow
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 template <int CH>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int slices) {
+__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, int slices) {
   constexpr int kAhead = 8 / CH;      // segments loaded ahead
   extern __shared__ float weights[];  // [segments][16]
   __shared__ float red[2][kJoinWorkers][kJoinRows];
@@ -1752,25 +1756,30 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
       }
       g = lo - 1;
     }
+    // all that the numbers of segments need is fetched before any is worked out
+    bool bad;
+    const Unit own = unit_at(p, p.G + t, bad);
+    const int64_t own_at = __ldcg(p.plan + 1 + p.G + t);
+    Unit x = own;
+    int64_t at = 0;
+    if (g >= 0) {
+      x = unit_at(p, g, bad);
+      at = __ldcg(p.plan + 1 + g);
+    }
     // CTAs c0 .. c1 have the row's key tiles
-    auto span = [&](const Unit& x, int64_t unit, int64_t tile, int rows, const uint8_t*& part, int& n) {
+    auto span = [&](const Unit& x, int64_t at, int64_t tile, int rows, const uint8_t*& part, int& n) {
       const int64_t per = x.row_cost();
       if (per == 0) return;
-      const int64_t f = __ldcg(p.plan + 1 + unit) + tile * per;
-      const int64_t c0 = (f + kCostSegment) / each, c1 = (f + per - x.tile_cost) / each;
+      const int64_t f = at + tile * per;
+      const int64_t c0 = quotient(f + x.start_cost, each), c1 = quotient(f + per - x.tile_cost, each);
       part += (c0 + x.part0 + tile) * part_bytes(rows);
       n = static_cast<int>(c1 - c0) + 1;
     };
-    bool bad;
-    const Unit own = unit_at(p, p.G + t, bad);
-    span(own, p.G + t, h / kRowsTile, p.own_rows, part2, n2);
-    if (g >= 0) {
-      const Unit x = unit_at(p, g, bad);
-      const int64_t i = t * p.H + h - x.rows0;
-      if (i >= 0 && i < x.rows) {
-        span(x, g, i / kRowsTile, kRowsTile, part1, n1);
-        row1 = static_cast<int>(i % kRowsTile);
-      }
+    span(own, own_at, h / kRowsTile, p.own_rows, part2, n2);
+    const int64_t i = t * p.H + h - x.rows0;
+    if (g >= 0 && i >= 0 && i < x.rows) {
+      span(x, at, i / kRowsTile, kRowsTile, part1, n1);
+      row1 = static_cast<int>(i % kRowsTile);
     }
   }
   const int n = n1 + n2;
@@ -1855,20 +1864,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
         acc[k].w += w * o[k].w;
       }
     };
-    int i = cls;
-    if (c0 == 0) {
+    for (int i = cls; i < n; i += kAhead * classes) {
+      if (c0 > 0 || i != cls) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j, i += classes)
-        if (i < n) add(i, ahead[j]);
-    }
-    for (; i < n; i += 4 * classes) {
-      float4 o[4][CH];
+        for (int j = 0; j < kAhead; ++j)
+          if (i + j * classes < n) load(i + j * classes, c0, ahead[j]);
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j * classes < n) load(i + j * classes, c0, o[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j * classes < n) add(i + j * classes, o[j]);
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * classes < n) add(i + j * classes, ahead[j]);
     }
     if (CH == 1 && classes > 1) {
       __syncthreads();
@@ -2141,10 +2145,10 @@ mla_status mla_prefix_attend_launch(
   s = launch(ks.attend, dim3(static_cast<unsigned>(sms), 1, 1), kThreads, ks.smem, pdl, stream, attend_args);
   if (s != MLA_OK) return s;
 
-  // slices: enough blocks for every SM to have some, a thread not below one chunk of columns
+  // slices: as many blocks as run at once, three to an SM, a thread not below one chunk of columns
   const int64_t rows = T * ((H + kJoinRows - 1) / kJoinRows);
   int32_t slices = 1;
-  while (slices < 32 && rows * slices < 2 * sms) slices *= 2;
+  while (slices < 32 && rows * slices * 2 <= 3 * sms) slices *= 2;
   void* jargs[] = {&p, &slices};
   const void* join = slices <= 2   ? reinterpret_cast<const void*>(&join_kernel<4>)
                      : slices == 4 ? reinterpret_cast<const void*>(&join_kernel<2>)
