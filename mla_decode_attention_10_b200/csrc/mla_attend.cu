@@ -150,7 +150,7 @@ constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
 // What the deal counts (measured cycles, in hundreds): a key tile, by how it comes,
 // and a segment's start and end, by its rows (their sums are written out).
-constexpr int kCostPrefix = 21, kCostRows = 27, kCostE4m3 = 56, kCostMx = 63, kCostF8 = 18, kCostSegment = 25, kCostRow = 1;
+constexpr int kCostPrefix = 21, kCostRows = 28, kCostE4m3 = 51, kCostMx = 60, kCostF8 = 18, kCostSegment = 25, kCostRow = 1;
 
 struct Params {
   const uint8_t* q;
@@ -203,6 +203,12 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// a / b; 64-bit divisions are slow
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // ---- units ---------------------------------------------------------------------
 
 struct Unit {
@@ -221,7 +227,7 @@ struct Unit {
   __device__ __forceinline__ int64_t row_cost() const { return len > 0 ? key_tiles() * tile_cost + start_cost : 0; }
   // the first key tile that starts at or behind position x of the row tile
   __device__ __forceinline__ int64_t tile_at(int64_t x) const {
-    return x > start_cost ? (x - start_cost + tile_cost - 1) / tile_cost : 0;
+    return x > start_cost ? quotient(x - start_cost + tile_cost - 1, tile_cost) : 0;
   }
   __device__ __forceinline__ int64_t cost() const { return row_tiles() * row_cost(); }
 };
@@ -325,7 +331,7 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
       c.known = nullptr;
       continue;
     }
-    const int64_t off = c.pos - c.base, r = off < per ? 0 : off / per, from = off - r * per;
+    const int64_t off = c.pos - c.base, r = off < per ? 0 : quotient(off, per), from = off - r * per;
     const int64_t to = per - from < c.end - c.pos ? per : from + (c.end - c.pos);
     c.pos += to - from;
     // the key tiles that start in this run
@@ -1193,10 +1199,15 @@ __device__ __forceinline__ void qk_rotary(uint32_t q_tmem, uint64_t q_smem, uint
 // STEPS 32-byte pieces of the q rows, at `q`, to TMEM from piece J0 on.
 template <int J0, int STEPS>
 __device__ __forceinline__ void q_copy(uint64_t q, uint32_t tmem) {
+  constexpr int kPieces = STEPS < 4 ? STEPS : 4;  // of a slab
+  uint32_t to = tmem + kTmemQ + 8u * J0;
+#pragma unroll 1
+  for (int s = 0; s < STEPS / kPieces; ++s) {
 #pragma unroll
-  for (int i = 0; i < 2 * STEPS; ++i)
-    tmem_copy(tmem + kTmemQ + 8u * J0 + 4u * static_cast<uint32_t>(i),
-              q + static_cast<uint64_t>((i >> 3) * (kSlabBytes >> 4) + (i & 7)));
+    for (int i = 0; i < 2 * kPieces; ++i) tmem_copy(to + 4u * static_cast<uint32_t>(i), q + static_cast<uint64_t>(i));
+    to += 32u;
+    q += kSlabBytes >> 4;
+  }
 }
 
 // Products issued by this warp have completed before TMEM is freed.
@@ -1545,7 +1556,7 @@ __device__ __forceinline__ Cursor plan_run(const Params& p, Shared& sh) {
   }
   // at least a tile's cost, so that every CTA between a row tile's first and last has one of its key tiles
   const int64_t least = p.tile_cost > p.prefix_cost ? p.tile_cost : p.prefix_cost;
-  const int64_t each = (total + p.ctas - 1) / p.ctas > least ? (total + p.ctas - 1) / p.ctas : least;
+  const int64_t even = quotient(total + p.ctas - 1, p.ctas), each = even > least ? even : least;
   Cursor c;
   c.pos = each * blockIdx.x;
   c.end = c.pos + each < total ? c.pos + each : total;
@@ -1714,12 +1725,6 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
 // and a row's segments shared out to classes of workers.
 
 constexpr int kJoinRows = 16, kJoinWorkers = 16, kJoinThreads = kJoinRows * kJoinWorkers;
-
-// a / b; 64-bit divisions are slow
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
 
 template <int CH>
 __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, int slices) {
