@@ -297,7 +297,10 @@ MLA_API mla_status mla_latent_gather_launch(
  *
  * Products run on the tensor cores with fp32 accumulation; scores, softmax
  * statistics and partial sums are fp32; the softmax weights are rounded to bf16
- * (to fp16 when both q and the cache are e4m3) before they multiply the keys.
+ * before they multiply the keys.  When both q and the cache are e4m3, the codes
+ * themselves are multiplied, and a weight is the sum of three e5m2 numbers (nine
+ * bits, one more than bf16's).  A product of q and a key beyond fp32's range is an
+ * infinity, and a row whose largest score is one comes out as NaN.
  *
  *   q       [T, H, 576] at element strides (q_stride_t, q_stride_h, 1): bf16, or e4m3
  *           bytes with MLA_FLAG_Q_FP8; 16-byte aligned, strides multiples of 16 bytes

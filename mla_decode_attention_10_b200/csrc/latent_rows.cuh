@@ -59,18 +59,6 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& c, float mul, uint4& 
   b.w = e4m3x2_to_bf16x2(c.w >> 16, mul);
 }
 
-// Sixteen codes -> sixteen fp16 (exact).
-__device__ __forceinline__ void codes_to_f16(const uint4& c, uint4& a, uint4& b) {
-  a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(c.x & 0xffffu));
-  a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(c.x >> 16));
-  a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(c.y & 0xffffu));
-  a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(c.y >> 16));
-  b.x = e4m3x2_to_f16x2(static_cast<uint16_t>(c.z & 0xffffu));
-  b.y = e4m3x2_to_f16x2(static_cast<uint16_t>(c.z >> 16));
-  b.z = e4m3x2_to_f16x2(static_cast<uint16_t>(c.w & 0xffffu));
-  b.w = e4m3x2_to_f16x2(static_cast<uint16_t>(c.w >> 16));
-}
-
 // 2^(byte - 127) of a scale byte as fp32; 255 is NaN.
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
   byte &= 0xffu;
@@ -79,9 +67,8 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
 
 // ---- the same conversions without the conversion unit, whose rate bounds a
 // kernel that decodes a tile per tile of products.  An e4m3 code s eeee mmm is,
-// bit for bit, a bf16 (fp16) number with its exponent 120 (8) too low, zeros
-// and subnormals included: one product with 2^120 (2^8), exact, puts that
-// right.  Only the NaN code (all ones) comes out as 480.
+// bit for bit, a bf16 number with its exponent 120 too low, zeros and subnormals
+// included: one product with 2^120, exact, puts that right.  Only the NaN code (all ones) comes out as 480.
 
 // Whether one of the sixteen codes is NaN.
 __device__ __forceinline__ bool any_nan_code(const uint4& c) {
@@ -96,19 +83,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // Four codes -> two words of 16-bit pairs before the product: each code in the
-// high byte of its half, exponent and mantissa shifted down by SHIFT.
-template <int SHIFT>
-__device__ __forceinline__ void spread_codes(uint32_t c, uint32_t mask, uint32_t& lo, uint32_t& hi) {
+// high byte of its half, exponent and mantissa shifted down by four.
+__device__ __forceinline__ void spread_codes(uint32_t c, uint32_t& lo, uint32_t& hi) {
   const uint32_t a = __byte_perm(c, 0u, 0x1404), b = __byte_perm(c, 0u, 0x3424);
-  lo = ((a >> SHIFT) & mask) | (a & 0x80008000u);
-  hi = ((b >> SHIFT) & mask) | (b & 0x80008000u);
+  lo = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+  hi = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
 }
 
 // Sixteen codes without a NaN times `mul2` = {m, m}, m = 2^120 times the scale (a power of two) in bf16.
@@ -118,24 +98,9 @@ __device__ __forceinline__ void plain_codes_to_bf16(const uint4& c, uint32_t mul
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t lo, hi;
-    spread_codes<4>(w[i], 0x07f007f0u, lo, hi);
+    spread_codes(w[i], lo, hi);
     o[2 * i] = mul_bf16x2(lo, mul2);
     o[2 * i + 1] = mul_bf16x2(hi, mul2);
-  }
-  a = make_uint4(o[0], o[1], o[2], o[3]);
-  b = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
-// Sixteen codes without a NaN -> fp16.
-__device__ __forceinline__ void plain_codes_to_f16(const uint4& c, uint4& a, uint4& b) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t lo, hi;
-    spread_codes<1>(w[i], 0x3f803f80u, lo, hi);
-    o[2 * i] = mul_f16x2(lo, 0x5c005c00u);  // 2^8
-    o[2 * i + 1] = mul_f16x2(hi, 0x5c005c00u);
   }
   a = make_uint4(o[0], o[1], o[2], o[3]);
   b = make_uint4(o[4], o[5], o[6], o[7]);

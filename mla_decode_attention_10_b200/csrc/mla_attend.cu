@@ -7,35 +7,54 @@
 // the prefix's keys) or a token (its H rows against its own keys).  A unit's
 // rows are taken 64 at a time (row tile) and its keys 64 at a time (key tile).
 // All (unit, row tile, key tile) triples, in this order, are dealt out to one
-// CTA per SM in equal contiguous runs: every CTA gets the same number of
-// tiles whatever the lengths are, and lengths stay in device memory (each CTA
-// adds them up itself).  A CTA's piece of one row tile is a segment; it ends
-// with the segment's unnormalised sum, maximum and denominator in the
-// workspace, and a second small kernel joins a row's segments.
+// CTA per SM in contiguous runs of equal cost, whatever the lengths are; lengths
+// stay in device memory (each CTA adds them up itself).  A CTA's piece of one row
+// tile is a segment; it ends with the segment's unnormalised sum, maximum and
+// denominator in the workspace, and a second kernel joins a row's segments.
 //
-// A CTA holds 64 rows because TMEM holds their fp32 sums, 64 x 512, in half of
-// its 512 columns (128 rows would fill it and leave no room for the scores).
-// M = 64 in the weight-stationary form (.ws) spreads a row over two TMEM lanes
-// (columns 0 .. N/2-1 on lanes 0..63, the rest on lanes 64..127).  Measured on
-// B200: N = 256 in 80 cycles, against 128 for the plain M = 64 form; N = 64 in
-// 50 for both.
+// Tensor cores.  A CTA holds 64 rows because TMEM holds their fp32 sums, 64 x 512,
+// in half of its 512 columns (128 rows would fill it and leave no room for the
+// scores).  M = 64 in the weight-stationary form (.ws) spreads a row over two TMEM
+// lanes (columns 0 .. N/2-1 on lanes 0..63, the rest on lanes 64..127).  Measured
+// on B200: N = 256 in 80 cycles, against 128 for the plain M = 64 form; N = 64 in
+// 32, or in 28 with the q rows in TMEM.  S = Q K^T is 36 such products a key tile
+// (N = 64, K = 16), O += P V is 8 (N = 256; V is the K tile itself, read with the
+// key index as the contraction): 1697 cycles in all.  With e4m3 q and cache the
+// codes are multiplied as they are (kind::f8f6f4, K = 32): 18 + 12 products (the
+// weights are three e5m2 terms), 1493 cycles.
 //
-// Roles (13 warps):
-//   warps 0..3   softmax: scores from TMEM, running maximum and sum, weights
-//                to shared memory, the sums' rescaling, the segment's result;
-//   warp 4       issues the MMAs: per key tile 36 of S = Q K^T (M 64, N 64,
-//                K 16) and 8 of O += P V (M 64, N 256, K 16; V is the K tile
-//                itself, read with the key index as the contraction);
-//   warps 5..12  load q and the cache rows, decode them to bf16 (or fp16 when
-//                both are e4m3: one conversion instead of four) and store
-//                them in the 128-byte swizzle.  The next tile's loads are in
-//                flight in registers while the tensor cores work on the two
-//                tiles in shared memory.  Plain loads take any block size,
-//                page order and row format, and zero what lies behind a
-//                sequence's end or in a page that does not exist.
+// Warps (16, one CTA an SM):
+//   softmax (8, or 4 where rows are decoded): scores from TMEM, running maximum
+//          and sum, weights to shared memory, the sums' rescaling (only when a
+//          row's maximum has grown by more than 2^8 since the last time), the
+//          segment's result;
+//   scores, sums (1 each): issue the products.  The queue of issued products is
+//          short: what one warp waits for between two products is lost time unless
+//          the other has some under way (one warp for both: 538 us instead of 492
+//          for 256 tokens over 32 K keys, all else the same);
+//   finder (1): looks up the CTA's segments for all the others;
+//   loaders (4, or 8 where rows are decoded) fill a ring of tile halves:
+//     - whole tiles of rows kept as they are (bf16; e4m3 with e4m3 q): tensor
+//       copies of 128 bytes x 8 to 64 rows, or of half a tile where a page has 64
+//       rows; one loader warp a tile, in turn;
+//     - tiles with a ragged end, or pages that tensor copies cannot follow:
+//       16-byte asynchronous copies, zeros where there is no key;
+//     - rows to be decoded: loads, integer arithmetic, stores;
+//     - prefixes of many rows that need decoding (or odd pages): decoded once by a
+//       kernel before this one, into images of tiles as they lie in shared memory,
+//       which come by two or three bulk copies.
 // S of tile i+1 is issued before O of tile i, so the softmax of i overlaps it.
 // Every wait is bounded: on timeout a status bit is set, all roles stop, TMEM
 // is freed and the kernel returns.
+//
+// What bounds it (cycles of a key tile, in the kernel): images and bf16 prefixes
+// 2070 to 2120, of which the products take 1697: the tile's way through the ring
+// (copy 1300, scores 1000, softmax 1300, sums 700) is longer than 2.5 tiles'
+// products; codes 1750 to 1850 of 1493, the softmax (one tile at a time, 900 for the
+// weights' three terms and 900 for the rest of the way round); a CTA's first bf16
+// tiles from HBM 2800.  Rows decoded by the loaders take 5100 (e4m3) to 6000 (mx):
+// the loads' latency (1200), which an arrival on a barrier does not let overlap the
+// stores of the tile before, then twice 1500 for a half's arithmetic and stores.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -119,9 +138,9 @@ struct Ring {
   }
 };
 
-// Roles.  Rows that need no decoding come by asynchronous copies, which four
-// warps issue easily, and leave eight warps for the softmax; decoding rows
-// takes eight warps.
+// Roles.  Rows that need no decoding are copied, which four warps issue easily,
+// and leave eight warps for the softmax (130 us with four, 115 with eight for 590 K
+// e4m3 keys, at the time); decoding rows takes eight warps.
 template <int FMT, int OP>
 struct Roles {
   static constexpr bool kDecode = OP == kBf16 && FMT != MLA_CACHE_BF16;
@@ -145,6 +164,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kTmemQ = 320;       // q rows: 32 bytes of each in 8 columns
 constexpr uint32_t kWaitSpins = 1u << 22;
+constexpr uint32_t kLandSpins = 1u << 14;  // for copies under way to land
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
@@ -378,7 +398,7 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn) {
 // everything that decides the addresses is uniform over it (broadcast where it
 // comes from memory), so the compiler keeps the descriptors in uniform
 // registers.  Issued from a branch on the lane, each MMA first moved its
-// descriptors there: 50 to 65 cycles, where the N = 64 form takes 32 (the 4 KB
+// descriptors there: 50 to 160 cycles, where the N = 64 form takes 32 (the 4 KB
 // of its operands at 128 bytes a cycle).
 template <int OP>
 __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -515,9 +535,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Waits for the phase, at most kWaitSpins tries or until another role gave up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  for (uint32_t i = 0; i < kWaitSpins; ++i) {
+// Waits for the phase, at most `spins` tries or until another role gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          uint32_t spins = kWaitSpins) {
+  for (uint32_t i = 0; i < spins; ++i) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -1129,7 +1150,7 @@ __device__ __forceinline__ void loader(const Params& p, const Maps& maps, Shared
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!good) {
     for (int i = 0; i < Shape<OP>::kHalves; ++i)
-      for (uint32_t parity = 0; parity < 2; ++parity) (void)warp_wait(smem_u32(&sh.bars.full[i]), parity, &sh.never);
+      for (uint32_t parity = 0; parity < 2; ++parity) (void)warp_wait(smem_u32(&sh.bars.full[i]), parity, &sh.never, kLandSpins);
   }
   if (!good) give_up(p, &sh.abort_flag);
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
@@ -1721,8 +1742,10 @@ __global__ void __launch_bounds__(256) image_kernel(const Params p) {
 // 16 of its heads and a slice of the columns; thread (row, worker), CH chunks of
 // four columns at a time.  A thread's first sums are loaded before the weights
 // they need are known, so the chain is plan, statistics and sums: few trips to
-// memory, whatever n is.  With few tokens the columns are cut into more slices
-// and a row's segments shared out to classes of workers.
+// memory, whatever n is (5 us: 1.9 for the plan, 1.3 for the statistics, the rest
+// for weights and sums).  With few tokens the columns are cut into more slices and
+// a row's segments shared out to classes of workers; all blocks run at once where
+// they can (1024 rows of 12 segments: in two waves 12 us, in one 6).
 
 constexpr int kJoinRows = 16, kJoinWorkers = 16, kJoinThreads = kJoinRows * kJoinWorkers;
 
@@ -1910,7 +1933,9 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
 // A prefix is decoded once, into the workspace, when its rows need decoding (or
 // pages are too small for tensor copies), its group has at least kImageRows rows
 // on average and the images fit kImageLimit; else its tiles are read from the
-// cache.
+// cache.  Measured with images and without: 128 rows behind 8 K mx keys 30 and 31
+// us, behind 32 K 54 and 47; 256 rows 33 and 37, 60 and 68; 1024 rows 45 and 69,
+// 107 and 189.
 constexpr int64_t kImageRows = 4 * kRowsTile;
 constexpr int kLeastBox = 8;  // rows of a tensor copy at least: the swizzle's period
 constexpr int64_t kImageLimit = INT64_C(1) << 31;

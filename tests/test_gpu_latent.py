@@ -645,3 +645,31 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for c, (o, l) in got:
         c.check(o, l)
+
+
+@pytest.mark.parametrize("fmt,q8", KINDS, ids=KIND_IDS)
+def test_attend_many_short_sequences(fmt, q8):
+    """A dozen or more pieces of work for every SM, of none to four tiles each, some behind a prefix."""
+    lens = [(53 * i) % 211 if i % 5 else 0 for i in range(1800)]
+    _run(_Case(fmt, 4, lens, prefixes=[70, 130], members=[0, 31, 900], block=32, q8=q8, seed=40))
+
+
+def test_attend_one_query_for_all_heads():
+    """Queries broadcast over the heads (stride 0)."""
+    case = _Case(R.BF16, 20, [70, 130], prefixes=[64], seed=41)
+    case.q = case.q[:, :1].expand(-1, 20, -1)
+    case.q64 = np.repeat(case.q64[:, :1], 20, axis=1)
+    out, _ = _run(case)
+    assert (out == out[:, :1]).all()
+
+
+@pytest.mark.parametrize("fmt,q8", KINDS, ids=KIND_IDS)
+def test_attend_the_same_pages_twice(fmt, q8):
+    """A sequence whose table names a page several times, and sequences that share their pages."""
+    for block in (16, 64):
+        case = _Case(fmt, 16, [2 * block, 4 * block + 5], block=block, q8=q8, seed=42)
+        pages, keys = case.table[0, :2].tolist(), case.keys[0]
+        order = [0, 0, 1, 0, 0]
+        case.table[1, :5] = torch.tensor([pages[i] for i in order], dtype=torch.int32)
+        case.keys[1] = np.concatenate([keys[i * block:(i + 1) * block] for i in order])[:4 * block + 5]
+        _run(case)
