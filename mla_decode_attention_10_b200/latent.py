@@ -113,12 +113,12 @@ def _launch(index: int, what: str, entry, *args) -> None:
         raise E.MlaError(rc, what)
 
 
-def _empty(shape: tuple, dtype: torch.dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _empty(index: int, stream: Optional[torch.cuda.Stream], dtype: torch.dtype, *shape: int) -> torch.Tensor:
     """Uninitialised memory that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=index)
+        return torch.empty(*shape, dtype=dtype, device=index)  # (0.8 us less than with the shape as a tuple)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=index)
+        return torch.empty(*shape, dtype=dtype, device=index)
 
 
 def mla_latent_cache_insert(
@@ -174,11 +174,15 @@ def mla_latent_cache_gather(
     st = None if status is None else _scalar("status", status, index, _I32)
     handle = _stream(stream, index).cuda_stream
     if out is None:
-        out = _empty((rows, E.ROW), _BF16, index, stream)
-    dst = _rows("out", out, index, _BF16, (rows, E.ROW))
+        if rows < 0:
+            raise ValueError("rows must not be negative")
+        out = _empty(index, stream, _BF16, rows, E.ROW)
+        dst, dst_stride = out.data_ptr(), E.ROW
+    else:
+        dst, dst_stride = _rows("out", out, index, _BF16, (rows, E.ROW)), out.stride(0)
     _launch(index, "mla_latent_gather_launch", E.lib().mla_latent_gather_launch,
             cache.data_ptr(), fmt, cache.shape[1], cache.shape[0], scale, table, table_stride, cols, cu, at, B, rows,
-            E.MLA_FLAG_PDL if pdl else 0, dst, out.stride(0), st, handle)
+            E.MLA_FLAG_PDL if pdl else 0, dst, dst_stride, st, handle)
     return out
 
 
@@ -220,7 +224,9 @@ def mla_prefix_decode_attention(
     index, fmt, scale = _cache(cache, kv_scale)
     if q.dim() != 3:
         raise ValueError("q must be [T, H, 576]")
-    T, H = q.shape[0], q.shape[1]
+    T, H, _ = q.shape
+    q_st, q_sh, _ = q.stride()
+    blocks, block, _ = cache.shape
     flags = E.MLA_FLAG_PDL if pdl else 0
     if q_scale is None:
         qp, qs = _rows("q", q, index, _BF16, (T, H, E.ROW)), None
@@ -247,16 +253,26 @@ def mla_prefix_decode_attention(
     st = None if status is None else _scalar("status", status, index, _I32)
     handle = _stream(stream, index).cuda_stream
     if out is None:
-        out = _empty((T, H, E.NOPE), _BF16, index, stream)
+        out = _empty(index, stream, _BF16, T, H, E.NOPE)
+        outp = out.data_ptr()
+    else:
+        outp = _flat("out", out, index, _BF16, (T, H, E.NOPE))
     if lse is None:
-        lse = _empty((T, H), _F32, index, stream)
+        lse = _empty(index, stream, _F32, T, H)
+        lsep = lse.data_ptr()
+    else:
+        lsep = _flat("lse", lse, index, _F32, (T, H))
     if workspace is None:
-        workspace = _empty((_workspace_bytes(T, H, G, pcols * cache.shape[1], _sm_count(index)),), _U8, index, stream)
+        nbytes = _workspace_bytes(T, H, G, pcols * block, _sm_count(index))
+        workspace = _empty(index, stream, _U8, nbytes)
+        ws = workspace.data_ptr()
     elif workspace.dim() != 1:
         raise ValueError("workspace must be a one-dimensional uint8 tensor")
+    else:
+        nbytes = workspace.numel()
+        ws = _flat("workspace", workspace, index, _U8, (nbytes,))
     _launch(index, "mla_prefix_attend_launch", E.lib().mla_prefix_attend_launch,
-            qp, q.stride(0), q.stride(1), qs, cache.data_ptr(), fmt, cache.shape[1], cache.shape[0], scale,
+            qp, q_st, q_sh, qs, cache.data_ptr(), fmt, block, blocks, scale,
             ptable, pstride, pcols, plens, offsets, G, table, table_stride, cols, lens, T, H, sm_scale, flags,
-            _flat("out", out, index, _BF16, (T, H, E.NOPE)), _flat("lse", lse, index, _F32, (T, H)),
-            _flat("workspace", workspace, index, _U8, tuple(workspace.shape)), workspace.numel(), st, handle)
+            outp, lsep, ws, nbytes, st, handle)
     return out, lse
