@@ -854,12 +854,14 @@ struct TileWalk {
   const int32_t* table = nullptr;
   int32_t len = 0, kt = 0, k0 = 0, k1 = 0;
   uint32_t seg = 0;    // segments begun
+  int32_t number = -1;  // of the tile, in the CTA's run
   int32_t owned = 0;   // tiles of the segment before this one are one warp's each
   bool copied = false;  // the segment's tiles come from an image
   bool any = true;     // not yet behind the last
 
   // To the next tile; false: a wait ran out.  `boxes`: tensor copies are made.
   __device__ __forceinline__ bool next(Shared& sh, bool boxes) {
+    ++number;
     if (!any || ++kt < k1) return true;
     if (!segment_known(sh, seg)) return false;
     const Segment& s = sh.segments[seg % kSegments];
@@ -889,7 +891,7 @@ struct Tile {
         first(w.kt == w.k0),
         any(w.any),
         whole(w.kt < w.owned),
-        mine(!(w.kt < w.owned) || (w.kt - w.k0) % warps == warp) {}
+        mine(!(w.kt < w.owned) || w.number % warps == warp) {}
 };
 
 // Where the key of row r of a tile lies.  The page number is fetched a tile
@@ -980,25 +982,36 @@ struct Maps {
 // half's barrier counts kArrivals of each warp: one of its own, and one of each
 // thread's asynchronous copies where there are any.
 template <int FMT, int OP>
-__device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Shared& sh, uint32_t smem,
-                                           bool& bad_page) {
+struct Filler {
   using S = Shape<OP>;
   using R = Roles<FMT, OP>;
-  constexpr bool kDecode = R::kDecode;
-  const int warp = uniform((static_cast<int>(threadIdx.x) >> 5) - R::kLoad0), lane = static_cast<int>(threadIdx.x) & 31;
-  const int row0 = R::kRows * warp;
-  volatile uint32_t* ab = &sh.abort_flag;
-  // Of a tile that all warps fill, lane i < kRows looks after row i of the warp's;
-  // of one that comes by tensor copies, lane i after box i, which is copied slab
-  // by slab.  Page numbers are fetched two tiles ahead.
-  TileWalk w;  // two tiles ahead of the one being stored
-  KeyAt at;
-  Raw<kDecode ? FMT : MLA_CACHE_E4M3> raw;
-  const int boxes = !kDecode && p.box_rows > 0 ? kKeys / p.box_rows : 0;
+  const Params& p;
+  Shared& sh;
+  uint32_t smem;
+  int warp, lane;
   Ring<OP> ring;
-  // the ring's next half, when it is free
-  auto acquire = [&]() { return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, ab); };
-  auto fill_q = [&](uint32_t seg) {
+
+  // The ring's next half, when it is free.
+  __device__ __forceinline__ bool acquire() const {
+    return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, &sh.abort_flag);
+  }
+  // Past a tile that is other warps' work.  Waits and arrives all the same: a wait on a
+  // barrier tells a phase from its neighbours only, so no warp may come to lag two
+  // phases behind the others.  (Without its arrivals a tile, the work of one warp,
+  // went its whole way without the rest.)
+  __device__ __forceinline__ bool skip_tile() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!acquire()) return false;
+      if (lane == 0) arrive(smem_u32(&sh.bars.full[ring.half]), kArrivals);
+      __syncwarp();
+      ring.next_half();
+    }
+    ring.next_tile();
+    return true;
+  }
+  // The q rows of segment seg - 1.
+  __device__ __forceinline__ bool fill_q(uint32_t seg) {
     const Segment& info = sh.segments[(seg - 1) % kSegments];
     const uint32_t full0 = smem_u32(&sh.bars.full[ring.half]), base0 = smem + ring.half * S::kHalf;
     if (!acquire()) return false;
@@ -1014,11 +1027,62 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Sh
              : s >= S::kHalfSlabs ? piece_addr(base1, s - S::kHalfSlabs, r, c)
                                   : piece_addr(base0, s, r, c);
     };
-    auto free = [&]() { return seg <= 1 || warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, ab); };
+    auto free = [&]() {
+      return seg <= 1 || warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, &sh.abort_flag);
+    };
     return load_q<FMT, OP>(p, info.row0, info.rows, to, free, full0, full1, warp, lane);
-  };
-  if (!w.next(sh, boxes > 0)) return false;
-  Tile now(w, warp, R::kLoad);
+  }
+  // A tile, half by half: put(h, place of a piece, barrier, place of the rotary slab, flags).
+  template <class Put>
+  __device__ __forceinline__ bool fill(const Put& put) {
+    const uint32_t pe = smem + S::kPeAt + ring.slot * kSlabBytes;
+    uint8_t* valid = sh.valid[ring.slot];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t full = smem_u32(&sh.bars.full[ring.half]), base = smem + ring.half * S::kHalf;
+      if (!acquire()) return false;
+      ring.next_half();
+      put(h, base, full, pe, valid);
+    }
+    ring.next_tile();
+    return true;
+  }
+  // A tile of an image.
+  __device__ __forceinline__ bool fill_image(const Tile& t) {
+    return fill([&](int h, uint32_t base, uint32_t full, uint32_t pe, uint8_t* valid) {
+      if (elect_one()) {
+        const uint8_t* image = sh.segments[(t.seg - 1) % kSegments].image + static_cast<int64_t>(t.kt) * S::kImage;
+        arrive(full, kArrivals - 1);
+        arrive_expect(full, S::kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
+        bulk_copy(base, image + h * S::kHalf, S::kHalf, full);
+        if (h == 0) {
+          bulk_copy(pe, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
+          bulk_copy(smem_u32(valid), image + S::kTile, kKeys, full);
+        }
+      }
+      __syncwarp();
+    });
+  }
+};
+
+// Piece `c` of slab `s`, row r of half h of a tile.
+template <int OP>
+__device__ __forceinline__ uint32_t half_addr(uint32_t base, uint32_t pe, int h, int s, int r, int c) {
+  return s == Shape<OP>::kPeSlab ? piece_addr(pe, 0, r, c) : piece_addr(base, s - h * Shape<OP>::kHalfSlabs, r, c);
+}
+
+// Rows kept as they are.
+template <int FMT, int OP>
+__device__ __forceinline__ bool copy_tiles(const Params& p, const Maps& maps, Filler<FMT, OP>& f, bool& bad_page) {
+  using S = Shape<OP>;
+  using R = Roles<FMT, OP>;
+  const int warp = f.warp, lane = f.lane, row0 = R::kRows * warp;
+  // Of a tile that all warps fill, lane i < kRows looks after row i of the warp's;
+  // of one that comes by tensor copies, lane i after box i, which is copied slab
+  // by slab.  Page numbers are fetched two tiles ahead.
+  TileWalk w;  // two tiles ahead of the one being stored
+  KeyAt at;
+  const int boxes = p.box_rows > 0 ? kKeys / p.box_rows : 0;
   auto fetch = [&](const Tile& t) {
     if (!t.any || !t.mine || t.copied) return;
     const int look = !t.whole ? (lane < R::kRows ? row0 + lane : -1) : lane < boxes ? lane * p.box_rows : -1;
@@ -1029,114 +1093,142 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Sh
   int32_t box = 0;
   auto locate = [&](const Tile& t) {
     mine = nullptr;
-    if (t.any && t.mine && !t.copied) {
-      mine = at.address(p, row_bytes(FMT), bad_page);
-      box = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
-    }
-    if constexpr (kDecode) load_rows<FMT>(raw, mine, lane);
+    if (!t.any || !t.mine || t.copied) return;
+    mine = at.address(p, row_bytes(FMT), bad_page);
+    box = static_cast<int32_t>(static_cast<uint32_t>(at.page) * static_cast<uint32_t>(p.block_size) + at.in_page);
   };
+  auto rows = [&](int h, uint32_t base, uint32_t full, uint32_t pe, uint8_t* valid) {
+    if (h == 0 && lane < R::kRows) valid[row0 + lane] = mine != nullptr ? 1 : 0;
+    const Pieces<OP, R::kRows> pieces(mine, lane);
+    auto copy = [&](int s, int r, int c, const uint8_t* src) {
+      cp_async16(half_addr<OP>(base, pe, h, s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
+    };
+    pieces.values(h, lane, copy);
+    if (h == 0) pieces.rotary(lane, copy);
+    cp_async_arrive(full);
+    __syncwarp();
+    if (lane == 0) arrive(full);
+  };
+  auto whole = [&](int h, uint32_t base, uint32_t full, uint32_t pe, uint8_t* valid) {
+    // a box in a page that does not exist: no keys
+    const uint32_t gone = __ballot_sync(0xffffffffu, lane < boxes && mine == nullptr);
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+    const int slabs = S::kHalfSlabs + (h == 0 ? 1 : 0);
+    if (h == 0 && lane < kKeys / 4) reinterpret_cast<uint32_t*>(valid)[lane] = 0x01010101u;
+    if (gone != 0u) {
+      __syncwarp();
+      if (h == 0 && lane < boxes && mine == nullptr)
+        for (int i = 0; i < p.box_rows; ++i) valid[lane * p.box_rows + i] = 0;
+      for (int i = lane; i < slabs * kKeys * 8; i += 32) {
+        const int s = i / (kKeys * 8), r = (i >> 3) % kKeys;
+        if ((gone >> (r / p.box_rows)) & 1u)
+          st_shared(half_addr<OP>(base, pe, h, s < S::kHalfSlabs ? h * S::kHalfSlabs + s : S::kPeSlab, r, i & 7),
+                    make_uint4(0, 0, 0, 0));
+      }
+      fence_async();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      arrive(full, kArrivals - 1);
+      arrive_expect(full, static_cast<uint32_t>(slabs * (boxes - __popc(gone))) * box_bytes);
+    }
+    __syncwarp();
+    if (lane < boxes && mine != nullptr) {
+      constexpr int kX = 128 / S::kElem;
+      const uint32_t row = static_cast<uint32_t>(lane) * box_bytes;
+      if (h == 0) tensor_copy(pe + row, maps.slab, S::kPeSlab * kX, box, full);
+      if (boxes == 1) {
+        tensor_copy_half(base, maps.half, box, h * S::kHalfSlabs, full);
+      } else {
+#pragma unroll
+        for (int s = 0; s < S::kHalfSlabs; ++s)
+          tensor_copy(base + static_cast<uint32_t>(s) * kSlabBytes + row, maps.slab, (h * S::kHalfSlabs + s) * kX, box, full);
+      }
+    }
+    __syncwarp();
+  };
+  auto next = [&]() { return w.next(f.sh, boxes > 0); };
+  auto tile = [&]() { return Tile(w, warp, R::kLoad); };
+  if (!next()) return false;
+  Tile now = tile();
   fetch(now);
   // the first segment's q rows go out while page numbers are under way
-  if (now.any && !fill_q(now.seg)) return false;
+  if (now.any && !f.fill_q(now.seg)) return false;
   locate(now);
-  if (!w.next(sh, boxes > 0)) return false;
-  Tile then(w, warp, R::kLoad);
+  if (!next()) return false;
+  Tile then = tile();
   fetch(then);
   while (now.any) {
-    if (now.first && now.seg > 1 && !fill_q(now.seg)) return false;
+    if (now.first && now.seg > 1 && !f.fill_q(now.seg)) return false;
     if (!now.mine) {
-      // waits all the same: a wait tells a phase from the one before, not from the one before that
-      ring.next_half();
-      if (!acquire()) return false;
-      ring.next_half();
-      ring.next_tile();
+      if (!f.skip_tile()) return false;
+    } else if (now.copied) {
+      if (!f.fill_image(now)) return false;
+    } else if (now.whole) {
+      if (!f.fill(whole)) return false;
     } else {
-      const uint32_t pe = smem + S::kPeAt + ring.slot * kSlabBytes;
-      uint8_t* valid = sh.valid[ring.slot];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t full = smem_u32(&sh.bars.full[ring.half]), base = smem + ring.half * S::kHalf;
-        if (!acquire()) return false;
-        ring.next_half();
-        auto to = [&](int s, int r, int c) {
-          return s == S::kPeSlab ? piece_addr(pe, 0, r, c) : piece_addr(base, s - h * S::kHalfSlabs, r, c);
-        };
-        if (!now.whole) {
-          if (h == 0 && lane < R::kRows) valid[row0 + lane] = mine != nullptr ? 1 : 0;
-          if constexpr (kDecode) {
-            store_half<FMT>(raw, h, row0, lane, [&](int s, int r, int c, const uint4& v) { st_shared(to(s, r, c), v); });
-          } else {
-            const Pieces<OP, R::kRows> pieces(mine, lane);
-            auto copy = [&](int s, int r, int c, const uint8_t* src) {
-              cp_async16(to(s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
-            };
-            pieces.values(h, lane, copy);
-            if (h == 0) pieces.rotary(lane, copy);
-            cp_async_arrive(full);
-          }
-          __syncwarp();
-          if (lane == 0) arrive(full, kDecode ? kArrivals : 1);
-        } else if (now.copied) {
-          if (elect_one()) {
-            const uint8_t* image = sh.segments[(now.seg - 1) % kSegments].image + static_cast<int64_t>(now.kt) * S::kImage;
-            arrive(full, kArrivals * R::kLoad - 1);
-            arrive_expect(full, S::kHalf + (h == 0 ? kSlabBytes + kKeys : 0));
-            bulk_copy(base, image + h * S::kHalf, S::kHalf, full);
-            if (h == 0) {
-              bulk_copy(pe, image + S::kPeSlab * kSlabBytes, kSlabBytes, full);
-              bulk_copy(smem_u32(valid), image + S::kTile, kKeys, full);
-            }
-          }
-          __syncwarp();
-        } else if constexpr (!kDecode) {
-          // a box in a page that does not exist: no keys
-          const uint32_t gone = __ballot_sync(0xffffffffu, lane < boxes && mine == nullptr);
-          const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
-          const int slabs = S::kHalfSlabs + (h == 0 ? 1 : 0);
-          if (h == 0 && lane < kKeys / 4) reinterpret_cast<uint32_t*>(valid)[lane] = 0x01010101u;
-          if (gone != 0u) {
-            __syncwarp();
-            if (h == 0 && lane < boxes && mine == nullptr)
-              for (int i = 0; i < p.box_rows; ++i) valid[lane * p.box_rows + i] = 0;
-            for (int i = lane; i < slabs * kKeys * 8; i += 32) {
-              const int s = i / (kKeys * 8), r = (i >> 3) % kKeys;
-              if ((gone >> (r / p.box_rows)) & 1u)
-                st_shared(to(s < S::kHalfSlabs ? h * S::kHalfSlabs + s : S::kPeSlab, r, i & 7), make_uint4(0, 0, 0, 0));
-            }
-            fence_async();
-          }
-          __syncwarp();
-          if (lane == 0) {
-            arrive(full, kArrivals * R::kLoad - 1);
-            arrive_expect(full, static_cast<uint32_t>(slabs * (boxes - __popc(gone))) * box_bytes);
-          }
-          __syncwarp();
-          if (lane < boxes && mine != nullptr) {
-            constexpr int kX = 128 / S::kElem;
-            const uint32_t row = static_cast<uint32_t>(lane) * box_bytes;
-            if (h == 0) tensor_copy(pe + row, maps.slab, S::kPeSlab * kX, box, full);
-            if (boxes == 1) {
-              tensor_copy_half(base, maps.half, box, h * S::kHalfSlabs, full);
-            } else {
-#pragma unroll
-              for (int s = 0; s < S::kHalfSlabs; ++s)
-                tensor_copy(base + static_cast<uint32_t>(s) * kSlabBytes + row, maps.slab, (h * S::kHalfSlabs + s) * kX, box,
-                            full);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      ring.next_tile();
+      if (!f.fill(rows)) return false;
     }
-    // (the next tile's rows, if they are decoded, behind this one's last arrival: an
-    // arrival waits for the loads before it)
     locate(then);
-    if (!then.any || then.first) segment_done(sh, now.seg - 1);
+    if (!then.any || then.first) segment_done(f.sh, now.seg - 1);
     now = then;
-    if (!w.next(sh, boxes > 0)) return false;
-    then = Tile(w, warp, R::kLoad);
+    if (!next()) return false;
+    then = tile();
     fetch(then);
+  }
+  return true;
+}
+
+// Rows to be decoded, eight a warp.  An arrival on a barrier waits for the loads
+// before it, so the next tile's go out behind this one's last arrival.  (Two groups
+// of four warps that take tiles in turn, sixteen rows a warp, so as to load and
+// decode at the same time, took 7200 and 6900 cycles a tile, against 6000 and 5100:
+// they too have to arrive for one another's tiles.)
+template <int FMT, int OP>
+__device__ __forceinline__ bool decode_tiles(const Params& p, Filler<FMT, OP>& f, bool& bad_page) {
+  using R = Roles<FMT, OP>;
+  constexpr int kRows = R::kRows;
+  const int warp = f.warp, lane = f.lane, row0 = kRows * warp;
+  TileWalk w;  // two tiles ahead of the one being stored
+  KeyAt at;
+  Raw<FMT> raw;
+  const uint8_t* mine = nullptr;  // the row that lane < kRows looks after
+  auto take = [&]() {
+    const Tile t(w, warp, R::kLoad);
+    if (t.any && !t.copied) at.fetch(p, w.table, w.len, t.kt, lane < kRows ? row0 + lane : -1, lane < kRows);
+    return t;
+  };
+  auto load = [&](const Tile& t) {
+    mine = t.any && !t.copied ? at.address(p, row_bytes(FMT), bad_page) : nullptr;
+    load_rows<FMT>(raw, mine, lane);
+  };
+  auto rows = [&](int h, uint32_t base, uint32_t full, uint32_t pe, uint8_t* valid) {
+    if (h == 0 && lane < kRows) valid[row0 + lane] = mine != nullptr ? 1 : 0;
+    store_half<FMT>(raw, h, row0, lane,
+                    [&](int s, int r, int c, const uint4& v) { st_shared(half_addr<OP>(base, pe, h, s, r, c), v); });
+    __syncwarp();
+    if (lane == 0) arrive(full, kArrivals);
+  };
+  if (!w.next(f.sh, false)) return false;
+  Tile now = take();
+  if (now.any && !f.fill_q(now.seg)) return false;
+  load(now);
+  if (!w.next(f.sh, false)) return false;
+  Tile then = take();
+  while (now.any) {
+    if (now.first && now.seg > 1 && !f.fill_q(now.seg)) return false;
+    if (!now.mine) {
+      if (!f.skip_tile()) return false;
+    } else if (now.copied) {
+      if (!f.fill_image(now)) return false;
+    } else {
+      if (!f.fill(rows)) return false;
+    }
+    load(then);
+    if (!then.any || then.first) segment_done(f.sh, now.seg - 1);
+    now = then;
+    if (!w.next(f.sh, false)) return false;
+    then = take();
   }
   return true;
 }
@@ -1144,7 +1236,15 @@ __device__ __forceinline__ bool load_tiles(const Params& p, const Maps& maps, Sh
 template <int FMT, int OP>
 __device__ __forceinline__ void loader(const Params& p, const Maps& maps, Shared& sh, uint32_t smem) {
   bool bad_page = false;
-  const bool good = load_tiles<FMT, OP>(p, maps, sh, smem, bad_page);
+  using R = Roles<FMT, OP>;
+  Filler<FMT, OP> f{p, sh, smem, uniform((static_cast<int>(threadIdx.x) >> 5) - R::kLoad0),
+                    static_cast<int>(threadIdx.x) & 31, {}};
+  bool good;
+  if constexpr (R::kDecode) {
+    good = decode_tiles<FMT, OP>(p, f, bad_page);
+  } else {
+    good = copy_tiles<FMT, OP>(p, maps, f, bad_page);
+  }
   // no copy may be under way when the CTA ends: on the way out after a timeout
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
