@@ -1455,7 +1455,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
   volatile uint32_t* ab = &sh.abort_flag;
   uint32_t it = 0;
   Ring<OP> ring;
-  bool good = true;
+  bool good = true;   // no wait has run out in this warp
+  bool left = false;  // the warps that share rows have left the walk together
   for (uint32_t segs = 0; good; ++segs) {
     good = segment_known(sh, segs);
     if (bar_or(bar_a, kShare, !good)) {  // the warps that share rows leave together
@@ -1519,6 +1520,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       if (moved) {
         if (bar_or(bar_b, kShare, !good)) {
           good = false;
+          left = true;
           break;
         }
         sh.xch[part][r] = top;
@@ -1599,9 +1601,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&sh.bars.p_full[buf]));
     }
-    if (!good) break;
+    if (left) break;
     // ---- the segment's result
-    good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab);
+    good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab) && good;
     if (bar_or(bar_a, kShare, !good)) {
       good = false;
       break;
