@@ -164,6 +164,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kTmemQ = 320;       // q rows: 32 bytes of each in 8 columns
 constexpr uint32_t kWaitSpins = 1u << 22;
+constexpr uint32_t kFindSpins = 1u << 26;  // for the next segment, behind millions of tokens without keys
 constexpr uint32_t kLandSpins = 1u << 14;  // for copies under way to land
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
@@ -336,12 +337,21 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
     } else if (c.u < p.G) {
       x = unit_at(p, c.u, bad);
     } else {
-      const int64_t t = c.u - p.G;
+      int64_t t = c.u - p.G;
+      if (t >= p.T) return false;  // (only if lengths change under the call)
       if (t - c.window >= 32) {
         const int64_t mine = t + (threadIdx.x & 31u);
         c.window = t;
         c.window_len = p.table_keys > 0 && mine < p.T ? __ldcg(p.seq_lens + mine) : 0;
       }
+      // to the next token that has keys of its own: the others count for nothing
+      const uint32_t some = __ballot_sync(0xffffffffu, c.window_len > 0) >> static_cast<int>(t - c.window);
+      if (some == 0u) {
+        c.u = p.G + c.window + 32;
+        continue;
+      }
+      t += __ffs(static_cast<int>(some)) - 1;
+      c.u = p.G + t;
       x = token_unit(p, t, __shfl_sync(0xffffffffu, c.window_len, static_cast<int>(t - c.window)), bad);
     }
     const int64_t per = x.row_cost(), n = x.row_tiles() * per;
@@ -840,7 +850,7 @@ __device__ __forceinline__ bool find_segments(const Params& p, Cursor cur, Share
 
 // Segment n, when it is known; and the warp's leave of it.
 __device__ __forceinline__ bool segment_known(Shared& sh, uint32_t n) {
-  return warp_wait(smem_u32(&sh.bars.seg_full[n % kSegments]), (n / kSegments) & 1u, &sh.abort_flag);
+  return warp_wait(smem_u32(&sh.bars.seg_full[n % kSegments]), (n / kSegments) & 1u, &sh.abort_flag, kFindSpins);
 }
 __device__ __forceinline__ void segment_done(Shared& sh, uint32_t n) {
   __syncwarp();
@@ -1901,7 +1911,9 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
       const int64_t per = x.row_cost();
       if (per == 0) return;
       const int64_t f = at + tile * per;
-      const int64_t c0 = quotient(f + x.start_cost, each), c1 = quotient(f + per - x.tile_cost, each);
+      // (cut, lest lengths that change under the call lead out of the workspace)
+      const int64_t c0 = cut(quotient(f + x.start_cost, each), 0, p.ctas - 1);
+      const int64_t c1 = cut(quotient(f + per - x.tile_cost, each), c0, p.ctas - 1);
       part += (c0 + x.part0 + tile) * part_bytes(rows);
       n = static_cast<int>(c1 - c0) + 1;
     };

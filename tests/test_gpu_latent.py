@@ -673,3 +673,55 @@ def test_attend_the_same_pages_twice(fmt, q8):
         case.table[1, :5] = torch.tensor([pages[i] for i in order], dtype=torch.int32)
         case.keys[1] = np.concatenate([keys[i * block:(i + 1) * block] for i in order])[:4 * block + 5]
         _run(case)
+
+
+def test_attend_long_stretches_of_tokens_without_keys():
+    """Half a million tokens, a few of which have keys."""
+    g = torch.Generator().manual_seed(43)
+    T, block = 500_000, 16
+    rows = _good_rows(g, 8 * block, R.BF16)
+    val = R.values(rows, R.BF16)
+    q = torch.zeros((T, 1, 576), dtype=torch.bfloat16, device="cuda")
+    lens = torch.zeros(T, dtype=torch.int32, device="cuda")
+    picked = [0, 1, 31, 70_000, 70_001, 400_032, T - 1]
+    some = _bf(g, len(picked), 1, 576)
+    for i, t in enumerate(picked):
+        lens[t], q[t] = 3 + 17 * i, some[i].cuda()
+    lens[5] = -4
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None].expand(T, 8)
+    out, lse = L.mla_prefix_decode_attention(q, _cache(rows, R.BF16, block), table, lens, sm_scale=0.07)
+    for i, t in enumerate(picked):
+        o, s, tol, stol = R.attend(some[i].double().numpy(), val[:3 + 17 * i], 0.07)
+        assert (np.abs(out[t].double().cpu().numpy() - o) <= tol).all(), t
+        assert (np.abs(lse[t].double().cpu().numpy() - s) <= stol).all(), t
+    lse[picked], out[picked] = float("-inf"), 0
+    assert (lse == float("-inf")).all() and (out == 0).all()
+
+
+@pytest.mark.parametrize("fmt,q8", [(R.BF16, False), (R.E4M3, True), (R.MX, False)], ids=["bf16", "e4m3", "mx"])
+def test_cache_of_more_than_32_bits(fmt, q8):
+    """Rows beyond byte 2^32 of the cache: written, read back and attended to."""
+    block, n = 64, 200
+    blocks = 2 ** 32 // (block * R.ROW_BYTES[fmt]) + 8
+    case = _Case(fmt, 16, [n], block=block, q8=q8, seed=44)
+    small = case.cache.view(torch.uint8).view(-1, block, R.ROW_BYTES[fmt])
+    big = torch.full((blocks, block, R.ROW_BYTES[fmt]), 0xFF, dtype=torch.uint8, device="cuda")
+    big[-small.shape[0]:] = small
+    assert (blocks - small.shape[0]) * block * R.ROW_BYTES[fmt] > 2 ** 32 - 2 ** 20
+    want = case.call()
+    near = L.mla_latent_cache_gather(case.cache, case.table[:, :4], torch.tensor([0, n], dtype=torch.int32, device="cuda"), n,
+                                     kv_scale=_kv_scale(fmt))
+    case.cache = big.view(torch.bfloat16) if fmt == R.BF16 else big
+    case.table[:, :4] += blocks - small.shape[0]
+    got = _run(case)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    far = L.mla_latent_cache_gather(case.cache, case.table[:, :4], torch.tensor([0, n], dtype=torch.int32, device="cuda"), n,
+                                    kv_scale=_kv_scale(fmt))
+    assert torch.equal(far.view(torch.int16), near.view(torch.int16))
+    x = _bf(torch.Generator().manual_seed(45), 3, 576).cuda()
+    slots = torch.arange(blocks * block - 3, blocks * block, device="cuda")
+    tiny = torch.zeros((1, block, R.ROW_BYTES[fmt]), dtype=torch.uint8, device="cuda")
+    tiny = tiny.view(torch.bfloat16) if fmt == R.BF16 else tiny
+    for cache, at in ((case.cache, slots), (tiny, torch.arange(3, device="cuda"))):
+        L.mla_latent_cache_insert(x[:, :512], x[:, 512:], cache, at, kv_scale=_kv_scale(fmt))
+    assert torch.equal(case.cache.view(torch.uint8)[-1, -3:], tiny.view(torch.uint8)[0, :3])
