@@ -24,6 +24,21 @@ __host__ __device__ constexpr int row_bytes(int format) {
   return format == MLA_CACHE_BF16 ? 1152 : format == MLA_CACHE_E4M3 ? 576 : kMxRow;
 }
 
+// 16 bytes, or zeros where there is no row; a predicate, not a branch, so that one
+// load need not have come before the next is issued.
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int at) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.s64 p, %4, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%5];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(row), "l"(row + at)
+      : "memory");
+  return v;
+}
+
 // Two e4m3 codes -> their values as fp16 (exact; NaN stays NaN), low code in the low half.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
   uint32_t r;

@@ -738,21 +738,6 @@ struct Raw {
   uint4 scales;  // mx: the 16 scale bytes of row `lane` (lanes 0..7)
 };
 
-// 16 bytes, or zeros where there is no row; a predicate, not a branch, so that one
-// load need not have come before the next is issued.
-__device__ __forceinline__ uint4 load16(const uint8_t* row, int at) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.s64 p, %4, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%5];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(row), "l"(row + at)
-      : "memory");
-  return v;
-}
-
 template <int FMT>
 __device__ __forceinline__ void load_rows(Raw<FMT>& raw, const uint8_t* mine, int lane) {
   const uint8_t* rows[4];

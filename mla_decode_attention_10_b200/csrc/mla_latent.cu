@@ -254,22 +254,19 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
       rows[i] = reinterpret_cast<const uint8_t*>(
           __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
     uint8_t* out = a.out + r0 * a.out_stride;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     if constexpr (FMT == MLA_CACHE_BF16) {
       // 72 pieces a row: 64 by all lanes, the other 8 of four rows at a time
 #pragma unroll
       for (int h = 0; h < kGatherRows; h += 4) {
-        uint4 x[8], y = zero;
+        const uint8_t* t = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), h + (lane >> 3)));
+        uint4 x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4* s = reinterpret_cast<const uint4*>(rows[h + i]);
-          if (s != nullptr) {
-            x[2 * i] = __ldcg(s + lane);
-            x[2 * i + 1] = __ldcg(s + 32 + lane);
-          }
+          x[2 * i] = load16(rows[h + i], 16 * lane);
+          x[2 * i + 1] = load16(rows[h + i], 512 + 16 * lane);
         }
-        const uint4* t = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), h + (lane >> 3)));
-        if (t != nullptr) y = __ldcg(t + 64 + (lane & 7));
+        const uint4 y = load16(t, 1024 + 16 * (lane & 7));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (rows[h + i] != nullptr) {
@@ -283,19 +280,18 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
     } else {
       uint4 c[kGatherRows];
       float scale = 1.0f;
-      uint4 scales = zero;  // mx: the 16 scale bytes of this lane's row
+      uint4 scales = make_uint4(0, 0, 0, 0);  // mx: the 16 scale bytes of this lane's row
       if constexpr (FMT == MLA_CACHE_E4M3) scale = __ldcg(a.kv_scale);
-      if constexpr (FMT == MLA_CACHE_MX)
-        if (src != nullptr) scales = __ldcg(reinterpret_cast<const uint4*>(src + kMxScales));
+      if constexpr (FMT == MLA_CACHE_MX) scales = load16(src, kMxScales);
 #pragma unroll
       for (int i = 0; i < kGatherRows; ++i)
-        c[i] = rows[i] != nullptr ? __ldcg(reinterpret_cast<const uint4*>(rows[i]) + lane) : zero;
+        c[i] = load16(rows[i], 16 * lane);
       if constexpr (FMT == MLA_CACHE_E4M3) {
         // the four last pieces of all eight rows
         const uint8_t* t = reinterpret_cast<const uint8_t*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), lane >> 2));
-        uint4 p = zero, x, y;
-        if (t != nullptr) p = __ldcg(reinterpret_cast<const uint4*>(t) + 32 + (lane & 3));
+        const uint4 p = load16(t, 512 + 16 * (lane & 3));
+        uint4 x, y;
         codes_to_bf16(p, scale, x, y);
         if (t != nullptr) store32(out + (lane >> 2) * a.out_stride + 1024 + 32 * (lane & 3), a.wide, x, y);
       } else {
@@ -304,8 +300,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
         for (int h = 0; h < 2; ++h) {
           const uint8_t* t = reinterpret_cast<const uint8_t*>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 4 * h + (lane >> 3)));
-          p[h] = zero;
-          if (t != nullptr) p[h] = __ldcg(reinterpret_cast<const uint4*>(t + kMxPe) + (lane & 7));
+          p[h] = load16(t, kMxPe + 16 * (lane & 7));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
