@@ -73,8 +73,9 @@ typedef enum mla_status {
                                     outside its block table, or group offsets that do not ascend: cut to what the
                                     table holds, or the row left out */
 #define MLA_STATUS_TIMEOUT    4  /* a bounded wait inside a kernel (on a copy, a barrier or the tensor cores)
-                                    ran out: the outputs are incomplete.  No such wait is expected ever to run
-                                    out; the kernel returns instead of hanging */
+                                    ran out: the outputs are incomplete (mla_prefix_attend_launch: the rows
+                                    concerned are NaN).  No such wait is expected ever to run out; the kernel
+                                    returns instead of hanging */
 
 /* Kernel choice (mla_plan.mode). */
 #define MLA_MODE_SPLIT 1 /* small T: three warps per 576-wide row (two move 16-byte nope chunks, one rotates the

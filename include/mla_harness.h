@@ -114,6 +114,15 @@ MLA_API mla_status mla_harness_consume(const void* q_out, const void* cache, con
                                        int64_t T, int64_t H, int64_t cache_rows, uint32_t flags, float* scores,
                                        mla_stream_t stream);
 
+/*
+ * How many times a wait inside mla_prefix_attend_launch's kernel is tried
+ * before it gives up with MLA_STATUS_TIMEOUT (in calls made from now on, by
+ * all threads; looked at every sixteenth try, some 20 ns each): a negative
+ * number or one beyond the default (2^22) restores the default.  For tests of
+ * that way out.
+ */
+MLA_API void mla_harness_attend_spins(int64_t spins);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,7 +45,8 @@
 //       which come by two or three bulk copies.
 // S of tile i+1 is issued before O of tile i, so the softmax of i overlaps it.
 // Every wait is bounded: on timeout a status bit is set, all roles stop, TMEM
-// is freed and the kernel returns.
+// is freed and the kernel returns.  Each CTA leaves word of it in the workspace,
+// and rows that it had a part in come out as NaN.
 //
 // What bounds it (cycles of a key tile, in the kernel): images and bf16 prefixes
 // 2070 to 2120, of which the products take 1697: the tile's way through the ring
@@ -68,6 +69,7 @@
 #include "latent_math.cuh"
 #include "latent_rows.cuh"
 #include "mla_epilogue.h"
+#include "mla_harness.h"
 #include "mla_runtime.h"
 
 namespace mla {
@@ -163,8 +165,8 @@ constexpr uint32_t kArrivals = 33;     // a loader warp's on a half's barrier: i
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;       // score buffers: columns 256 + 32 b
 constexpr uint32_t kTmemQ = 320;       // q rows: 32 bytes of each in 8 columns
-constexpr uint32_t kWaitSpins = 1u << 22;
-constexpr uint32_t kFindSpins = 1u << 26;  // for the next segment, behind millions of tokens without keys
+constexpr uint32_t kWaitSpins = 1u << 22;  // tries of a wait
+constexpr uint32_t kFindTimes = 16;        // that many more for the next segment, behind millions of tokens without keys
 constexpr uint32_t kLandSpins = 1u << 14;  // for copies under way to land
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
 constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
@@ -194,6 +196,7 @@ struct Params {
   uint16_t* out;
   float* lse;
   int64_t* plan;      // [0] each CTA's run, [1 + u] where unit u starts
+  uint32_t* gave_up;  // by CTA: 1 if one of its waits ran out, and its segments are not to be trusted
   uint8_t* image;     // decoded prefix tiles, or null: prefixes are read from the cache
   int64_t image_tiles;  // tiles of one group's image
   uint8_t* prefix_part;
@@ -203,6 +206,7 @@ struct Params {
   int32_t image_bytes;  // of one tile's image
   int32_t box_rows;     // cache rows of one tensor copy (8, 16, 32 or 64), or 0: none are made
   int32_t tile_cost, prefix_cost;  // of a tile of own keys, of a prefix
+  uint32_t spins;     // tries of a wait: kWaitSpins, or fewer in tests
   int32_t* status;
 };
 
@@ -545,10 +549,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Waits for the phase, at most `spins` tries or until another role gave up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                          uint32_t spins = kWaitSpins) {
-  for (uint32_t i = 0; i < spins; ++i) {
+// Waits for the phase, until `spins` tries (looked at every sixteenth) or another role's giving up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t spins) {
+  for (uint32_t i = 0;; ++i) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -560,9 +563,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
         : "r"(bar), "r"(parity)
         : "memory");
     if (__any_sync(0xffffffffu, done != 0u)) return true;
-    if ((i & 15u) == 15u && __any_sync(0xffffffffu, *abort_flag != 0u)) return false;
+    if ((i & 15u) == 15u && __any_sync(0xffffffffu, i >= spins || *abort_flag != 0u)) return false;
   }
-  return false;
 }
 
 // barrier `id` over `n` threads, returning the OR of `pred` over them
@@ -822,7 +824,7 @@ __device__ __forceinline__ bool find_segments(const Params& p, Cursor cur, Share
     Segment s;
     if (!next_segment(p, cur, s)) s.k0 = s.k1 = 0;
     if (n >= kSegments &&
-        !warp_wait(smem_u32(&sh.bars.seg_empty[n % kSegments]), (n / kSegments - 1) & 1u, &sh.abort_flag))
+        !warp_wait(smem_u32(&sh.bars.seg_empty[n % kSegments]), (n / kSegments - 1) & 1u, &sh.abort_flag, p.spins))
       return false;
     if ((threadIdx.x & 31u) == 0u) {
       sh.segments[n % kSegments] = s;
@@ -834,8 +836,8 @@ __device__ __forceinline__ bool find_segments(const Params& p, Cursor cur, Share
 }
 
 // Segment n, when it is known; and the warp's leave of it.
-__device__ __forceinline__ bool segment_known(Shared& sh, uint32_t n) {
-  return warp_wait(smem_u32(&sh.bars.seg_full[n % kSegments]), (n / kSegments) & 1u, &sh.abort_flag, kFindSpins);
+__device__ __forceinline__ bool segment_known(const Params& p, Shared& sh, uint32_t n) {
+  return warp_wait(smem_u32(&sh.bars.seg_full[n % kSegments]), (n / kSegments) & 1u, &sh.abort_flag, kFindTimes * p.spins);
 }
 __device__ __forceinline__ void segment_done(Shared& sh, uint32_t n) {
   __syncwarp();
@@ -855,10 +857,10 @@ struct TileWalk {
   bool any = true;     // not yet behind the last
 
   // To the next tile; false: a wait ran out.  `boxes`: tensor copies are made.
-  __device__ __forceinline__ bool next(Shared& sh, bool boxes) {
+  __device__ __forceinline__ bool next(const Params& p, Shared& sh, bool boxes) {
     ++number;
     if (!any || ++kt < k1) return true;
-    if (!segment_known(sh, seg)) return false;
+    if (!segment_known(p, sh, seg)) return false;
     const Segment& s = sh.segments[seg % kSegments];
     kt = k0 = uniform(s.k0);
     k1 = uniform(s.k1);
@@ -988,7 +990,7 @@ struct Filler {
 
   // The ring's next half, when it is free.
   __device__ __forceinline__ bool acquire() const {
-    return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, &sh.abort_flag);
+    return ring.lap == 0 || warp_wait(smem_u32(&sh.bars.empty[ring.half]), (ring.lap - 1) & 1u, &sh.abort_flag, p.spins);
   }
   // Past a tile that is other warps' work.  Waits and arrives all the same: a wait on a
   // barrier tells a phase from its neighbours only, so no warp may come to lag two
@@ -1023,7 +1025,7 @@ struct Filler {
                                   : piece_addr(base0, s, r, c);
     };
     auto free = [&]() {
-      return seg <= 1 || warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, &sh.abort_flag);
+      return seg <= 1 || warp_wait(smem_u32(&sh.bars.q_empty), (seg - 2) & 1u, &sh.abort_flag, p.spins);
     };
     return load_q<FMT, OP>(p, info.row0, info.rows, to, free, full0, full1, warp, lane);
   }
@@ -1142,7 +1144,7 @@ __device__ __forceinline__ bool copy_tiles(const Params& p, const Maps& maps, Fi
     }
     __syncwarp();
   };
-  auto next = [&]() { return w.next(f.sh, boxes > 0); };
+  auto next = [&]() { return w.next(p, f.sh, boxes > 0); };
   auto tile = [&]() { return Tile(w, warp, R::kLoad); };
   if (!next()) return false;
   Tile now = tile();
@@ -1204,11 +1206,11 @@ __device__ __forceinline__ bool decode_tiles(const Params& p, Filler<FMT, OP>& f
     __syncwarp();
     if (lane == 0) arrive(full, kArrivals);
   };
-  if (!w.next(f.sh, false)) return false;
+  if (!w.next(p, f.sh, false)) return false;
   Tile now = take();
   if (now.any && !f.fill_q(now.seg)) return false;
   load(now);
-  if (!w.next(f.sh, false)) return false;
+  if (!w.next(p, f.sh, false)) return false;
   Tile then = take();
   while (now.any) {
     if (now.first && now.seg > 1 && !f.fill_q(now.seg)) return false;
@@ -1222,7 +1224,7 @@ __device__ __forceinline__ bool decode_tiles(const Params& p, Filler<FMT, OP>& f
     load(then);
     if (!then.any || then.first) segment_done(f.sh, now.seg - 1);
     now = then;
-    if (!w.next(f.sh, false)) return false;
+    if (!w.next(p, f.sh, false)) return false;
     then = take();
   }
   return true;
@@ -1244,10 +1246,10 @@ __device__ __forceinline__ void loader(const Params& p, const Maps& maps, Shared
   // (else every copy's tile has been used) give the copy engine's theirs
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!good) {
+    give_up(p, &sh.abort_flag);
     for (int i = 0; i < Shape<OP>::kHalves; ++i)
       for (uint32_t parity = 0; parity < 2; ++parity) (void)warp_wait(smem_u32(&sh.bars.full[i]), parity, &sh.never, kLandSpins);
   }
-  if (!good) give_up(p, &sh.abort_flag);
   if (bad_page) report(p.status, MLA_STATUS_SLOT_RANGE);
 }
 
@@ -1329,12 +1331,12 @@ __device__ __forceinline__ void q_copy(uint64_t q, uint32_t tmem) {
 // Products issued by this warp have completed before TMEM is freed.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t* never) {
   commit(smem_u32(bar));
-  (void)warp_wait(smem_u32(bar), 0u, never);
+  (void)warp_wait(smem_u32(bar), 0u, never, kWaitSpins);
 }
 
 // Issues the copies of every segment's q rows to TMEM and the scores' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ bool issue_scores(const Params& p, Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t d_half = smem_desc(smem, 16, 1024), d_pe = smem_desc(smem + S::kPeAt, 16, 1024);
@@ -1346,13 +1348,13 @@ __device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t
   // stores or asynchronous copies and the tensor cores' reads is made here: made by
   // the warps that decode rows, it waited for the next rows' loads.)
   auto come = [&]() {
-    if (!warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab)) return false;
+    if (!warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab, p.spins)) return false;
     fence_async();
     fence_after();
     return true;
   };
   while (true) {
-    if (!segment_known(sh, segs)) return false;
+    if (!segment_known(p, sh, segs)) return false;
     const Segment& x = sh.segments[segs % kSegments];
     const int tiles = uniform(x.k1 - x.k0);
     if (tiles == 0) return true;
@@ -1360,7 +1362,7 @@ __device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t
     if (!come()) return false;
     // The products that read the previous segment's q rows have completed.  Those
     // that read these run behind the copies.
-    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.q_empty), (segs - 1) & 1u, ab)) return false;
+    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.q_empty), (segs - 1) & 1u, ab, p.spins)) return false;
     ++segs;
     q_copy<0, 4 * S::kHalfSlabs>(smem_desc(smem + ring.half * S::kHalf, 16, 1024), tmem);
     if (S::kPeSlab < S::kQSlab0)
@@ -1376,7 +1378,7 @@ __device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t
     for (int i = 0; i < tiles; ++i, ++it) {
       const uint32_t buf = it & 1u;
       const uint32_t d = tmem + kTmemS + 32u * buf;
-      if (it >= 2 && !warp_wait(smem_u32(&sh.bars.s_empty[buf]), (it / 2 - 1) & 1u, ab)) return false;
+      if (it >= 2 && !warp_wait(smem_u32(&sh.bars.s_empty[buf]), (it / 2 - 1) & 1u, ab, p.spins)) return false;
       if (!come()) return false;
       qk_rotary<OP>(q + 32u * S::kPeSlab, d_q + static_cast<uint64_t>(S::kQSlabs > 0 ? (S::kQSlabs - 1) * (kSlabBytes >> 4) : 0),
                     d_pe + ring.slot * (kSlabBytes >> 4), d);
@@ -1396,24 +1398,24 @@ __device__ __forceinline__ bool issue_scores(Shared& sh, uint32_t smem, uint32_t
 
 // Issues the sums' products of every tile.
 template <int OP>
-__device__ __forceinline__ bool issue_sums(Shared& sh, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ bool issue_sums(const Params& p, Shared& sh, uint32_t smem, uint32_t tmem) {
   using S = Shape<OP>;
   volatile uint32_t* ab = &sh.abort_flag;
   const uint64_t d_p = smem_desc(smem + S::kPAt, 16, 1024), d_v = smem_desc(smem, kSlabBytes, 1024);
   uint32_t it = 0, segs = 0;
   Ring<OP> ring;
   while (true) {
-    if (!segment_known(sh, segs)) return false;
+    if (!segment_known(p, sh, segs)) return false;
     const Segment& x = sh.segments[segs % kSegments];
     const int tiles = uniform(x.k1 - x.k0);
     if (tiles == 0) return true;
     segment_done(sh, segs);
     ring.skip_tile();  // the q rows
-    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.o_empty), (segs - 1) & 1u, ab)) return false;
+    if (segs > 0 && !warp_wait(smem_u32(&sh.bars.o_empty), (segs - 1) & 1u, ab, p.spins)) return false;
     ++segs;
     for (int i = 0; i < tiles; ++i, ++it) {
       const uint32_t buf = it & 1u;
-      if (!warp_wait(smem_u32(&sh.bars.p_full[buf]), (it / 2) & 1u, ab)) return false;
+      if (!warp_wait(smem_u32(&sh.bars.p_full[buf]), (it / 2) & 1u, ab, p.spins)) return false;
       fence_async();  // the weights came by plain stores (and the rows may have)
       fence_after();
       const uint64_t w = d_p + (S::kPBufs > 1 ? buf * (S::kP >> 4) : 0u);
@@ -1453,7 +1455,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
   bool good = true;   // no wait has run out in this warp
   bool left = false;  // the warps that share rows have left the walk together
   for (uint32_t segs = 0; good; ++segs) {
-    good = segment_known(sh, segs);
+    good = segment_known(p, sh, segs);
     if (bar_or(bar_a, kShare, !good)) {  // the warps that share rows leave together
       good = false;
       break;
@@ -1467,7 +1469,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
       const uint32_t buf = it & 1u;
       // the flags first: they are there before the scores, and may have come by the copy engine
-      good = warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab) && good;
+      good = warp_wait(smem_u32(&sh.bars.full[ring.half]), ring.lap & 1u, ab, p.spins) && good;
       uint32_t ok[kN / 4];
 #pragma unroll
       for (int j = 0; j < kN / 16; ++j) {
@@ -1481,7 +1483,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
 #pragma unroll
       for (int j = 1; j < kN / 4; ++j) all &= ok[j];
       const bool whole = all == 0x01010101u;
-      good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab) && good;
+      good = warp_wait(smem_u32(&sh.bars.s_full[buf]), (it / 2) & 1u, ab, p.spins) && good;
       fence_after();
       uint32_t v[kN];
       tmem_ld<kN>(tmem + kTmemS + 32u * buf + lanes + static_cast<uint32_t>(sub * kN), v);
@@ -1562,10 +1564,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // the weights that were in this buffer have been read
       constexpr uint32_t kBack = Shape<OP>::kPBufs;
-      if (it >= kBack) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - kBack) & 1u]), ((it - kBack) / 2) & 1u, ab);
+      if (it >= kBack) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - kBack) & 1u]), ((it - kBack) / 2) & 1u, ab, p.spins);
       if (moved && !first) {
         // the previous tile's products are in the sums (all threads move or none)
-        if (kBack > 1) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab) && good;
+        if (kBack > 1) good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab, p.spins) && good;
         fence_after();
 #pragma unroll 1
         for (uint32_t c = 0; c < 1024u / WARPS; c += 32) {
@@ -1598,7 +1600,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
     }
     if (left) break;
     // ---- the segment's result
-    good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab) && good;
+    good = warp_wait(smem_u32(&sh.bars.pv_done[(it - 1) & 1u]), ((it - 1) / 2) & 1u, ab, p.spins) && good;
     if (bar_or(bar_a, kShare, !good)) {
       good = false;
       break;
@@ -1770,10 +1772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
       if (warp == R::kScores) {
-        if (!issue_scores<OP>(sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        if (!issue_scores<OP>(p, sh, smem, tmem)) give_up(p, &sh.abort_flag);
         drain(&sh.bars.drained[0], &sh.never);
       } else if (warp == R::kSums) {
-        if (!issue_sums<OP>(sh, smem, tmem)) give_up(p, &sh.abort_flag);
+        if (!issue_sums<OP>(p, sh, smem, tmem)) give_up(p, &sh.abort_flag);
         drain(&sh.bars.drained[1], &sh.never);
       } else if (warp == R::kFinds) {
         if (!find_segments(p, cur, sh)) give_up(p, &sh.abort_flag);
@@ -1782,6 +1784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) p.gave_up[blockIdx.x] = sh.abort_flag;
   if (warp == R::kScores) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -1869,6 +1872,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
   const uint8_t* part2 = p.own_part;
   int row1 = 0;
   const int row2 = h % kRowsTile;
+  int cta1 = 0, cta2 = 0;  // the CTA that has its first segment of either kind; the others follow
   if (live) {
     int64_t g = -1;
     if (p.G > 0 && p.group_offsets == nullptr) {
@@ -1892,7 +1896,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
       at = __ldcg(p.plan + 1 + g);
     }
     // CTAs c0 .. c1 have the row's key tiles
-    auto span = [&](const Unit& x, int64_t at, int64_t tile, int rows, const uint8_t*& part, int& n) {
+    auto span = [&](const Unit& x, int64_t at, int64_t tile, int rows, const uint8_t*& part, int& cta, int& n) {
       const int64_t per = x.row_cost();
       if (per == 0) return;
       const int64_t f = at + tile * per;
@@ -1900,12 +1904,13 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
       const int64_t c0 = cut(quotient(f + x.start_cost, each), 0, p.ctas - 1);
       const int64_t c1 = cut(quotient(f + per - x.tile_cost, each), c0, p.ctas - 1);
       part += (c0 + x.part0 + tile) * part_bytes(rows);
+      cta = static_cast<int>(c0);
       n = static_cast<int>(c1 - c0) + 1;
     };
-    span(own, own_at, h / kRowsTile, p.own_rows, part2, n2);
+    span(own, own_at, h / kRowsTile, p.own_rows, part2, cta2, n2);
     const int64_t i = t * p.H + h - x.rows0;
     if (g >= 0 && i >= 0 && i < x.rows) {
-      span(x, at, i / kRowsTile, kRowsTile, part1, n1);
+      span(x, at, i / kRowsTile, kRowsTile, part1, cta1, n1);
       row1 = static_cast<int>(i % kRowsTile);
     }
   }
@@ -1947,6 +1952,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
   // ---- weights
   float m0 = -INFINITY, l0 = 0.0f;
   if (wk < n) stats_of(wk, m0, l0);
+  for (int i = wk; i < n; i += kJoinWorkers)  // what a CTA left that gave up may be an earlier call's: the row is NaN
+    if (__ldcg(p.gave_up + (i < n1 ? cta1 + i : cta2 + i - n1)) != 0u) l0 = __uint_as_float(0x7fffffffu);
   float top = m0;
   for (int i = wk + kJoinWorkers; i < n; i += kJoinWorkers) {
     float m, l;
@@ -2040,7 +2047,7 @@ constexpr int kLeastBox = 8;  // rows of a tensor copy at least: the swizzle's p
 constexpr int64_t kImageLimit = INT64_C(1) << 31;
 
 struct Layout {
-  int64_t prefix_part, own_part, image, image_tiles, bytes;
+  int64_t gave_up, prefix_part, own_part, image, image_tiles, bytes;
 };
 
 // (The bf16 image's size: the caller need not know which operands a call takes.)
@@ -2048,7 +2055,8 @@ Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t c
   constexpr int64_t kImageBytes = Shape<kBf16>::kImage;
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout l;
-  l.prefix_part = up(8 * (1 + G + T));
+  l.gave_up = 8 * (1 + G + T);
+  l.prefix_part = up(l.gave_up + 4 * ctas);
   const int64_t prefix_parts = G > 0 ? T * H / kRowsTile + G + 1 + ctas : 0;
   l.own_part = up(l.prefix_part + prefix_parts * part_bytes(kRowsTile));
   const int64_t own_parts = T * ((H + kRowsTile - 1) / kRowsTile) + ctas;
@@ -2080,6 +2088,7 @@ const Kernels kKernels[4] = {kernels_of<MLA_CACHE_BF16, kBf16>(kCostRows), kerne
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 std::atomic<bool> g_smem_ready[kMaxDevices][4];
+std::atomic<uint32_t> g_spins{kWaitSpins};  // (mla_harness_attend_spins)
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
@@ -2131,6 +2140,11 @@ mla_status launch(const void* fn, dim3 grid, int threads, size_t smem, bool pdl,
 }  // namespace mla
 
 extern "C" {
+
+void mla_harness_attend_spins(int64_t spins) {
+  using namespace mla::attend;
+  g_spins.store(spins < 0 || spins > kWaitSpins ? kWaitSpins : static_cast<uint32_t>(spins), std::memory_order_relaxed);
+}
 
 mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t sm_count,
                                        int64_t* bytes) {
@@ -2213,12 +2227,14 @@ mla_status mla_prefix_attend_launch(
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.plan = reinterpret_cast<int64_t*>(ws);
+  p.gave_up = reinterpret_cast<uint32_t*>(ws + lay.gave_up);
   p.image = lay.image_tiles > 0 ? ws + lay.image : nullptr;
   p.image_tiles = lay.image_tiles;
   p.prefix_part = ws + lay.prefix_part;
   p.own_part = ws + lay.own_part;
   p.own_rows = static_cast<int32_t>(H < kRowsTile ? H : kRowsTile);
   p.ctas = sms;
+  p.spins = g_spins.load(std::memory_order_relaxed);
   p.status = status;
 
   const int k = format == MLA_CACHE_E4M3 && q8 ? 3 : format;

@@ -120,6 +120,8 @@ def lib() -> ctypes.CDLL:
         L.mla_prefix_attend_launch.argtypes = [vp, i64, i64, vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64,
                                                vp, i64, i64, vp, i64, i64, ctypes.c_float, u32, vp, vp, vp, i64,
                                                vp, vp]
+        L.mla_harness_attend_spins.restype = None
+        L.mla_harness_attend_spins.argtypes = [i64]
         L.mla_harness_div_check.restype = ctypes.c_int
         L.mla_harness_div_check.argtypes = [ctypes.c_float, u64, u64, vp, vp]
         L.mla_harness_bf16_scale_check.restype = ctypes.c_int
@@ -181,6 +183,11 @@ def mla_harness_produce_after_weights(src_nope, src_pe, q_nope, q_nope_stride_t,
     return lib().mla_harness_produce_after_weights(src_nope, src_pe, q_nope, q_nope_stride_t, q_nope_stride_h, q_pe,
                                                    q_pe_stride_t, q_pe_stride_h, weights, weight_bytes, sink, T, H,
                                                    flags, stream)
+
+
+def mla_harness_attend_spins(spins: int = -1) -> None:
+    """Tries of a wait in mla_prefix_attend_launch before it gives up (default: as shipped)."""
+    lib().mla_harness_attend_spins(spins)
 
 
 def mla_harness_empty(blocks: int, threads: int, flags: int, stream) -> int:

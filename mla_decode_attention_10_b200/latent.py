@@ -219,7 +219,8 @@ def mla_prefix_decode_attention(
     with one group: every token).  Without ``prefix_table`` there are no
     prefixes.  A ``workspace`` (uint8, at least ``mla_prefix_attend_workspace``
     bytes) must not be shared by calls that may run at the same time; without
-    one each call takes its own.
+    one each call takes its own.  Rows whose computation a timeout cut short
+    (``MLA_STATUS_TIMEOUT`` in ``status``) are NaN.
     """
     index, fmt, scale = _cache(cache, kv_scale)
     if q.dim() != 3:
