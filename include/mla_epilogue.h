@@ -300,7 +300,9 @@ MLA_API mla_status mla_latent_gather_launch(
  * statistics and partial sums are fp32; the softmax weights are rounded to bf16
  * before they multiply the keys.  When both q and the cache are e4m3, the codes
  * themselves are multiplied, and a weight is the sum of three e5m2 numbers (nine
- * bits, one more than bf16's).  A product of q and a key beyond fp32's range is an
+ * bits, one more than bf16's; what weights too small for that lose is together at
+ * most 2^-11 of the denominator, or 2^-30 for each key of a token where those are
+ * more).  A product of q and a key beyond fp32's range is an
  * infinity, and a row whose largest score is one comes out as NaN.
  *
  *   q       [T, H, 576] at element strides (q_stride_t, q_stride_h, 1): bf16, or e4m3

@@ -26,7 +26,7 @@
 // Warps (16, one CTA an SM):
 //   softmax (8, or 4 where rows are decoded): scores from TMEM, running maximum
 //          and sum, weights to shared memory, the sums' rescaling (only when a
-//          row's maximum has grown by more than 2^8 since the last time), the
+//          row's maximum has grown by more than a margin since the last time), the
 //          segment's result;
 //   scores, sums (1 each): issue the products.  The queue of issued products is
 //          short: what one warp waits for between two products is lost time unless
@@ -169,7 +169,6 @@ constexpr uint32_t kWaitSpins = 1u << 22;  // tries of a wait
 constexpr uint32_t kFindTimes = 16;        // that many more for the next segment, behind millions of tokens without keys
 constexpr uint32_t kLandSpins = 1u << 14;  // for copies under way to land
 constexpr float kRescale = 8.0f;       // the reference maximum moves when a score passes it by 2^8
-constexpr float kF8Lift = 7.0f;        // kF8 weights are 2^7 times p: at most 2^15, e5m2 reaches 57344 and 2^-16
 constexpr int kChunks = kDv / 4;       // 16-byte pieces of a row's fp32 sums
 // What the deal counts (measured cycles, in hundreds): a key tile, by how it comes,
 // and a segment's start and end, by its rows (their sums are written out).
@@ -209,6 +208,18 @@ struct Params {
   uint32_t spins;     // tries of a wait: kWaitSpins, or fewer in tests
   int32_t* status;
 };
+
+// kF8 weights are 2^lift times p, at most 2^15: e5m2 reaches 57344, and down to
+// 2^-16, so each is off by up to 2^-17 / 2^lift of the largest.  All of n keys
+// that is n times as much, and the denominator does not share it: the lift is the
+// one at which it stays below 2^-11, 7 up to 2^13 keys and one more for each
+// doubling, up to 13 (2^19 keys).  The reference may lag behind a row's maximum by
+// what is left of 15.  (Not 13 for all: 590 K e4m3 keys, 4 K a CTA, take 98 us with
+// 7 and 8 left, 101 with 12 and 3, 103 with 13 and 2.)
+constexpr float kF8Top = 15.0f;
+__device__ __forceinline__ float f8_lift(int tiles) {
+  return fminf(static_cast<float>(7 + 32 - __clz(max(tiles - 1, 0) >> 7)), 13.0f);
+}
 
 // ---- a segment's result: fp32 sums as [chunk of 4 columns][row] 16-byte
 // pieces (neighbouring rows, on neighbouring lanes, are contiguous), then the
@@ -1463,6 +1474,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
     const Segment seg = sh.segments[segs % kSegments];
     if (seg.k0 == seg.k1) break;
     segment_done(sh, segs);
+    const float lift = OP == kF8 ? f8_lift(seg.k1 - seg.k0) : 0.0f;
+    const float margin = OP == kF8 ? kF8Top - lift : kRescale;
     float m = -INFINITY;  // the reference maximum of the row, in powers of two
     float l = 0.0f;       // this thread's share of the denominator
     ring.skip_tile();     // the q rows
@@ -1512,7 +1525,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       const bool first = kt == seg.k0;
       // One vote a tile: whether a row's reference must move, or a wait ran out
       // (then all the warps leave together).
-      const bool moved = bar_or(bar_a, kShare, first || top > m + kRescale || !good);
+      const bool moved = bar_or(bar_a, kShare, first || top > m + margin || !good);
       float factor = 1.0f;
       if (moved) {
         if (bar_or(bar_b, kShare, !good)) {
@@ -1529,7 +1542,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
         m = next;
         l *= factor;
       }
-      const float ref = (m == -INFINITY ? 0.0f : m) - (OP == kF8 ? kF8Lift : 0.0f);
+      const float ref = (m == -INFINITY ? 0.0f : m) - lift;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       uint32_t w[kN / 2], mid[kN / 4], lo[kN / 4];
 #pragma unroll
@@ -1632,7 +1645,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       float den = l;
 #pragma unroll
       for (int i = 1; i < kParts; ++i) den += sh.xch[i][r];
-      __stcg(stat + r, OP == kF8 ? (m == -INFINITY ? m : m - kF8Lift) : m);
+      __stcg(stat + r, OP == kF8 ? (m == -INFINITY ? m : m - lift) : m);
       __stcg(stat + seg.part_rows + r, den);
     }
     bar_sync(bar_b, kShare);
