@@ -303,7 +303,8 @@ MLA_API mla_status mla_latent_gather_launch(
  * bits, one more than bf16's; what weights too small for that lose is together at
  * most 2^-11 of the denominator, or 2^-30 for each key of a token where those are
  * more).  A product of q and a key beyond fp32's range is an
- * infinity, and a row whose largest score is one comes out as NaN.
+ * infinity, and a row whose largest score is one comes out as NaN.  So may a row
+ * whose largest score is beyond 2^30 in magnitude, or 2^27 with q and cache in e4m3.
  *
  *   q       [T, H, 576] at element strides (q_stride_t, q_stride_h, 1): bf16, or e4m3
  *           bytes with MLA_FLAG_Q_FP8; 16-byte aligned, strides multiples of 16 bytes

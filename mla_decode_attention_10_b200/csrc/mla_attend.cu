@@ -217,6 +217,13 @@ struct Params {
 // what is left of 15.  (Not 13 for all: 590 K e4m3 keys, 4 K a CTA, take 98 us with
 // 7 and 8 left, 101 with 12 and 3, 103 with 13 and 2.)
 constexpr float kF8Top = 15.0f;
+// A score's scale and its difference to the reference are one rounding, but the
+// reference has been rounded too, by half a unit: that far the largest weight may
+// be from 1.  Where the unit passes 1, kF8 weights go without lift and margin; where
+// it would lead out of a weight's type, the row is NaN.
+constexpr float kF8Large = 4194304.0f;                       // 2^22
+constexpr float kF8Most = 268435456.0f;                       // 2^28: off by 2^8 at most
+constexpr float kMost = 2147483648.0f;                       // 2^31: by 2^64
 __device__ __forceinline__ float f8_lift(int tiles) {
   return fminf(static_cast<float>(7 + 32 - __clz(max(tiles - 1, 0) >> 7)), 13.0f);
 }
@@ -1475,8 +1482,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
     if (seg.k0 == seg.k1) break;
     segment_done(sh, segs);
     const float lift = OP == kF8 ? f8_lift(seg.k1 - seg.k0) : 0.0f;
-    const float margin = OP == kF8 ? kF8Top - lift : kRescale;
-    float m = -INFINITY;  // the reference maximum of the row, in powers of two
+    float m = -INFINITY;      // the row's maximum when the reference last moved, in powers of two
+    float ref = 0.0f;         // the reference
+    float limit = -INFINITY;  // it moves when a score passes this
     float l = 0.0f;       // this thread's share of the denominator
     ring.skip_tile();     // the q rows
     for (int kt = seg.k0; kt < seg.k1; ++kt, ++it) {
@@ -1525,7 +1533,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       const bool first = kt == seg.k0;
       // One vote a tile: whether a row's reference must move, or a wait ran out
       // (then all the warps leave together).
-      const bool moved = bar_or(bar_a, kShare, first || top > m + margin || !good);
+      const bool moved = bar_or(bar_a, kShare, first || top > limit || !good);
       float factor = 1.0f;
       if (moved) {
         if (bar_or(bar_b, kShare, !good)) {
@@ -1538,11 +1546,21 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
         float next = m;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) next = fmaxf(next, sh.xch[i][r]);
-        if (!first && next > m) factor = m == -INFINITY ? 0.0f : exp2_fast(m - next);
-        m = next;
+        if (next > m) {
+          float next_ref = next;
+          limit = next + kRescale;
+          if constexpr (OP == kF8) {
+            const bool large = fabsf(next) >= kF8Large;
+            next_ref = large ? next : next - lift;
+            limit = large ? next : next + (kF8Top - lift);
+          }
+          if (fabsf(next) >= (OP == kF8 ? kF8Most : kMost)) next_ref = __uint_as_float(0x7fffffffu);
+          if (!first) factor = m == -INFINITY ? 0.0f : exp2_fast(ref - next_ref);
+          m = next;
+          ref = next_ref;
+        }
         l *= factor;
       }
-      const float ref = (m == -INFINITY ? 0.0f : m) - lift;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       uint32_t w[kN / 2], mid[kN / 4], lo[kN / 4];
 #pragma unroll
@@ -1645,7 +1663,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       float den = l;
 #pragma unroll
       for (int i = 1; i < kParts; ++i) den += sh.xch[i][r];
-      __stcg(stat + r, OP == kF8 ? (m == -INFINITY ? m : m - lift) : m);
+      __stcg(stat + r, m == -INFINITY ? m : ref);
       __stcg(stat + seg.part_rows + r, den);
     }
     bar_sync(bar_b, kShare);
