@@ -316,8 +316,11 @@ MLA_API mla_status mla_latent_gather_launch(
  *   block_table int32 [T, table_cols] at row stride table_stride; seq_lens int32 [T].
  *           table_cols == 0 (block_table NULL): no token has keys of its own
  *   out     bf16 [T, H, 512] contiguous, 16-byte aligned;  lse fp32 [T, H] or NULL
- *   workspace  mla_prefix_attend_workspace() bytes (prefix_keys = prefix_cols *
- *           block_size; sm_count 0: of the current device) of device memory,
+ *   workspace  mla_prefix_attend_workspace_for() bytes (prefix_keys = prefix_cols *
+ *           block_size; sm_count 0: of the current device) of device memory;
+ *           mla_prefix_attend_workspace() bytes are enough for every cache.  Large
+ *           groups over rows that need decoding take 73856 bytes for each 64 keys of
+ *           prefix_keys, up to 2 GiB, the others none;
  *           256-byte aligned; need not be initialised, holds nothing between calls;
  *           two calls that may run at the same time need two
  *   flags   MLA_FLAG_Q_FP8, MLA_FLAG_PDL (everything is read after the wait)
@@ -328,6 +331,9 @@ MLA_API mla_status mla_latent_gather_launch(
  */
 MLA_API mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t sm_count,
                                                int64_t* bytes);
+MLA_API mla_status mla_prefix_attend_workspace_for(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t format,
+                                                   uint32_t flags, int64_t block_size, int64_t num_blocks,
+                                                   int32_t sm_count, int64_t* bytes);
 
 MLA_API mla_status mla_prefix_attend_launch(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, const float* q_scale,

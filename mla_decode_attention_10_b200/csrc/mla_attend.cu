@@ -2081,9 +2081,11 @@ struct Layout {
   int64_t gave_up, prefix_part, own_part, image, image_tiles, bytes;
 };
 
-// (The bf16 image's size: the caller need not know which operands a call takes.)
-Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t ctas) {
-  constexpr int64_t kImageBytes = Shape<kBf16>::kImage;
+// `image_bytes`: of a tile's image, 0 where a call makes none.  (How many tiles may
+// be imaged goes by the largest images, whatever a call's are, so that a workspace
+// for those is enough for every call.)
+constexpr int32_t kMostImageBytes = static_cast<int32_t>(Shape<kBf16>::kImage);
+Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t ctas, int64_t image_bytes) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout l;
   l.gave_up = 8 * (1 + G + T);
@@ -2093,8 +2095,9 @@ Layout layout_of(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int64_t c
   const int64_t own_parts = T * ((H + kRowsTile - 1) / kRowsTile) + ctas;
   l.image = up(l.own_part + own_parts * part_bytes(static_cast<int>(H < kRowsTile ? H : kRowsTile)));
   l.image_tiles = (prefix_keys + kKeys - 1) / kKeys;
-  if (G < 1 || G > 65535 || T * H < kImageRows * G || l.image_tiles > kImageLimit / kImageBytes / G) l.image_tiles = 0;
-  l.bytes = up(l.image + G * l.image_tiles * kImageBytes);
+  if (image_bytes == 0 || G < 1 || G > 65535 || T * H < kImageRows * G || l.image_tiles > kImageLimit / kMostImageBytes / G)
+    l.image_tiles = 0;
+  l.bytes = up(l.image + G * l.image_tiles * image_bytes);
   return l;
 }
 
@@ -2146,6 +2149,23 @@ int box_rows_of(int64_t block_size) {
   return r >= kLeastBox ? r : 0;
 }
 
+// The kernels a call takes, and whether they fetch whole tiles by tensor copies: rows of
+// 16-bit values or codes as they are, in pages of a multiple of eight rows.
+int kernels_at(int32_t format, bool q8) { return format == MLA_CACHE_E4M3 && q8 ? 3 : format; }
+bool needs_decoding(int k) { return k == MLA_CACHE_MX || k == MLA_CACHE_E4M3; }
+bool by_tensor_copies(int k, int64_t block_size, int64_t num_blocks) {
+  const int64_t cache_rows = num_blocks * block_size;
+  return !needs_decoding(k) && box_rows_of(block_size) > 0 && cache_rows > 0 && cache_rows < INT_MAX;
+}
+int64_t image_bytes_of(int k, int64_t block_size, int64_t num_blocks) {
+  return by_tensor_copies(k, block_size, num_blocks) ? 0 : kKernels[k].image_bytes;
+}
+
+bool cache_ok(int32_t format, int64_t block_size, int64_t num_blocks) {
+  return format >= MLA_CACHE_BF16 && format <= MLA_CACHE_MX && block_size >= 1 && block_size <= INT_MAX && num_blocks >= 0 &&
+         num_blocks <= (INT64_C(1) << 50) / block_size;
+}
+
 bool sizes_ok(int64_t T, int64_t H, int64_t G) {
   return T >= 0 && H >= 1 && H <= 65535 && T <= (static_cast<int64_t>(INT_MAX) - kRowsTile) / H && G >= 0 && G <= T;
 }
@@ -2186,7 +2206,24 @@ mla_status mla_prefix_attend_workspace(int64_t T, int64_t H, int64_t G, int64_t 
     const mla_status s = mla::current_device(nullptr, &sm_count);
     if (s != MLA_OK) return s;
   }
-  *bytes = layout_of(T, H, G, prefix_keys, sm_count).bytes;
+  *bytes = layout_of(T, H, G, prefix_keys, sm_count, kMostImageBytes).bytes;
+  return MLA_OK;
+}
+
+mla_status mla_prefix_attend_workspace_for(int64_t T, int64_t H, int64_t G, int64_t prefix_keys, int32_t format, uint32_t flags,
+                                           int64_t block_size, int64_t num_blocks, int32_t sm_count, int64_t* bytes) {
+  using namespace mla::attend;
+  if ((flags & ~(MLA_FLAG_Q_FP8 | MLA_FLAG_PDL)) != 0 || format < MLA_CACHE_BF16 || format > MLA_CACHE_MX)
+    return MLA_ERR_UNSUPPORTED;
+  if (bytes == nullptr || !sizes_ok(T, H, G) || prefix_keys < 0 || prefix_keys > (INT64_C(1) << 62) ||
+      !cache_ok(format, block_size, num_blocks))
+    return MLA_ERR_INVALID_ARG;
+  if (sm_count <= 0) {
+    const mla_status s = mla::current_device(nullptr, &sm_count);
+    if (s != MLA_OK) return s;
+  }
+  const int k = kernels_at(format, (flags & MLA_FLAG_Q_FP8) != 0);
+  *bytes = layout_of(T, H, G, prefix_keys, sm_count, image_bytes_of(k, block_size, num_blocks)).bytes;
   return MLA_OK;
 }
 
@@ -2201,10 +2238,9 @@ mla_status mla_prefix_attend_launch(
   using namespace mla::attend;
   if ((flags & ~(MLA_FLAG_Q_FP8 | MLA_FLAG_PDL)) != 0) return MLA_ERR_UNSUPPORTED;
   if (format < MLA_CACHE_BF16 || format > MLA_CACHE_MX) return MLA_ERR_UNSUPPORTED;
-  if (!sizes_ok(T, H, G) || block_size < 1 || block_size > INT_MAX || num_blocks < 0 || table_cols < 0 ||
-      table_cols > INT_MAX || table_stride < 0 || prefix_cols < 0 || prefix_cols > INT_MAX || prefix_stride < 0)
+  if (!sizes_ok(T, H, G) || !cache_ok(format, block_size, num_blocks) || table_cols < 0 || table_cols > INT_MAX ||
+      table_stride < 0 || prefix_cols < 0 || prefix_cols > INT_MAX || prefix_stride < 0)
     return MLA_ERR_INVALID_ARG;
-  if (num_blocks > (INT64_C(1) << 50) / block_size) return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
   if (T == 0) return MLA_OK;
   const bool q8 = (flags & MLA_FLAG_Q_FP8) != 0;
@@ -2227,7 +2263,8 @@ mla_status mla_prefix_attend_launch(
   int32_t sms = 0;
   mla_status s = mla::current_device(&dev, &sms);
   if (s != MLA_OK) return s;
-  const Layout lay = layout_of(T, H, G, prefix_cols * block_size, sms);
+  const int k = kernels_at(format, q8);
+  const Layout lay = layout_of(T, H, G, prefix_cols * block_size, sms, image_bytes_of(k, block_size, num_blocks));
   if (workspace_bytes < lay.bytes) return MLA_ERR_INVALID_ARG;
 
   Params p;
@@ -2268,7 +2305,6 @@ mla_status mla_prefix_attend_launch(
   p.spins = g_spins.load(std::memory_order_relaxed);
   p.status = status;
 
-  const int k = format == MLA_CACHE_E4M3 && q8 ? 3 : format;
   const Kernels& ks = kKernels[k];
   p.image_bytes = ks.image_bytes;
   p.tile_cost = ks.tile_cost;
@@ -2279,13 +2315,11 @@ mla_status mla_prefix_attend_launch(
     if (e != cudaSuccess) return mla::cuda_failure(e);
     g_smem_ready[dev][k].store(true, std::memory_order_release);
   }
-  // Tensor copies: rows of 16-bit values or codes as they are, in pages of a multiple of eight rows
   CUtensorMap slab_map{}, half_map{};
   p.box_rows = 0;
-  const bool decode = k == MLA_CACHE_MX || k == MLA_CACHE_E4M3;
-  const int64_t cache_rows = num_blocks * block_size;
-  const int box = box_rows_of(block_size);
-  if (!decode && box > 0 && cache_rows > 0 && cache_rows < INT_MAX) {
+  if (by_tensor_copies(k, block_size, num_blocks)) {
+    const int64_t cache_rows = num_blocks * block_size;
+    const int box = box_rows_of(block_size);
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return mla::cuda_failure(cudaErrorNotSupported);
     const cuuint64_t elem = k == 3 ? 1 : 2;
@@ -2306,9 +2340,8 @@ mla_status mla_prefix_attend_launch(
     }
     if (r != CUDA_SUCCESS) return MLA_ERR_INVALID_ARG;
     p.box_rows = box;
-    p.image = nullptr;
   }
-  p.prefix_cost = decode && p.image == nullptr ? ks.tile_cost : ks.prefix_cost;
+  p.prefix_cost = needs_decoding(k) && p.image == nullptr ? ks.tile_cost : ks.prefix_cost;
   void* args[] = {&p};
   void* attend_args[] = {&slab_map, &half_map, &p};
   bool pdl = (flags & MLA_FLAG_PDL) != 0;

@@ -116,6 +116,8 @@ def lib() -> ctypes.CDLL:
                                                vp, vp]
         L.mla_prefix_attend_workspace.restype = ctypes.c_int
         L.mla_prefix_attend_workspace.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(i64)]
+        L.mla_prefix_attend_workspace_for.restype = ctypes.c_int
+        L.mla_prefix_attend_workspace_for.argtypes = [i64, i64, i64, i64, i32, u32, i64, i64, i32, ctypes.POINTER(i64)]
         L.mla_prefix_attend_launch.restype = ctypes.c_int
         L.mla_prefix_attend_launch.argtypes = [vp, i64, i64, vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64,
                                                vp, i64, i64, vp, i64, i64, ctypes.c_float, u32, vp, vp, vp, i64,
@@ -231,12 +233,23 @@ def mla_latent_gather_launch(cache, format, block_size, num_blocks, kv_scale, bl
 
 
 def mla_prefix_attend_workspace(T: int, H: int, G: int, prefix_keys: int = 0, sm_count: int = 0) -> int:
-    """Bytes of workspace mla_prefix_attend_launch needs (prefix_keys: pages of a prefix table row times the block
-    size; sm_count 0: of the current device)."""
+    """Bytes of workspace that are enough for mla_prefix_attend_launch on any cache (prefix_keys: pages of a prefix
+    table row times the block size; sm_count 0: of the current device)."""
     n = ctypes.c_int64()
     rc = lib().mla_prefix_attend_workspace(T, H, G, prefix_keys, sm_count, ctypes.byref(n))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_prefix_attend_workspace")
+    return n.value
+
+
+def mla_prefix_attend_workspace_for(T: int, H: int, G: int, prefix_keys: int, format: int, flags: int, block_size: int,
+                                    num_blocks: int, sm_count: int = 0) -> int:
+    """Bytes of workspace mla_prefix_attend_launch needs for a cache of this format (flags: MLA_FLAG_Q_FP8 or 0)."""
+    n = ctypes.c_int64()
+    rc = lib().mla_prefix_attend_workspace_for(T, H, G, prefix_keys, format, flags, block_size, num_blocks, sm_count,
+                                               ctypes.byref(n))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_prefix_attend_workspace_for")
     return n.value
 
 

@@ -196,7 +196,7 @@ def _sm_count(index: int) -> int:
     return n
 
 
-_workspace_bytes = functools.lru_cache(maxsize=256)(E.mla_prefix_attend_workspace)
+_workspace_bytes = functools.lru_cache(maxsize=256)(E.mla_prefix_attend_workspace_for)
 
 
 def mla_prefix_decode_attention(
@@ -217,8 +217,8 @@ def mla_prefix_decode_attention(
     of their own).  ``prefix_table`` is int32 [G, pages]; group g holds the
     tokens ``group_offsets[g] .. group_offsets[g + 1] - 1`` (int32 [G + 1]; None
     with one group: every token).  Without ``prefix_table`` there are no
-    prefixes.  A ``workspace`` (uint8, at least ``mla_prefix_attend_workspace``
-    bytes) must not be shared by calls that may run at the same time; without
+    prefixes.  A ``workspace`` (uint8, at least ``mla_prefix_attend_workspace_for``
+    bytes, or ``mla_prefix_attend_workspace`` for any cache) must not be shared by calls that may run at the same time; without
     one each call takes its own.  Rows whose computation a timeout cut short
     (``MLA_STATUS_TIMEOUT`` in ``status``) are NaN.
     """
@@ -264,7 +264,7 @@ def mla_prefix_decode_attention(
     else:
         lsep = _flat("lse", lse, index, _F32, (T, H))
     if workspace is None:
-        nbytes = _workspace_bytes(T, H, G, pcols * block, _sm_count(index))
+        nbytes = _workspace_bytes(T, H, G, pcols * block, fmt, flags & E.MLA_FLAG_Q_FP8, block, blocks, _sm_count(index))
         workspace = _empty(index, stream, _U8, nbytes)
         ws = workspace.data_ptr()
     elif workspace.dim() != 1:
