@@ -379,8 +379,18 @@ __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Segment
     const int64_t per = x.row_cost(), n = x.row_tiles() * per;
     if (c.pos >= c.base + n) {
       c.base += n;
-      ++c.u;
       c.known = nullptr;
+      uint32_t u = static_cast<uint32_t>(c.u) + 1u;
+      const uint32_t groups = static_cast<uint32_t>(p.G);
+      if (n == 0 && u < groups) {  // past groups without keys or tokens, 32 at a time (so there are offsets)
+        const uint32_t mine = u + (threadIdx.x & 31u);
+        bool works = true;
+        if (mine < groups)
+          works = __ldcg(p.prefix_lens + mine) > 0 && __ldcg(p.group_offsets + mine) < __ldcg(p.group_offsets + mine + 1);
+        const uint32_t some = __ballot_sync(0xffffffffu, works);
+        u += some != 0u ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 32u;
+      }
+      c.u = u;
       continue;
     }
     const int64_t off = c.pos - c.base, r = off < per ? 0 : quotient(off, per), from = off - r * per;
