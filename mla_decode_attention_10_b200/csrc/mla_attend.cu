@@ -1126,7 +1126,7 @@ __device__ __forceinline__ bool copy_tiles(const Params& p, const Maps& maps, Fi
     if (h == 0 && lane < R::kRows) valid[row0 + lane] = mine != nullptr ? 1 : 0;
     const Pieces<OP, R::kRows> pieces(mine, lane);
     auto copy = [&](int s, int r, int c, const uint8_t* src) {
-      cp_async16(half_addr<OP>(base, pe, h, s, row0 + r, c), src != nullptr ? src : p.cache, src != nullptr);
+      cp_async16(half_addr<OP>(base, pe, h, s, row0 + r, c), src != nullptr ? src : p.q, src != nullptr);
     };
     pieces.values(h, lane, copy);
     if (h == 0) pieces.rotary(lane, copy);
@@ -2254,7 +2254,7 @@ mla_status mla_prefix_attend_launch(
   if (!std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
   if (T == 0) return MLA_OK;
   const bool q8 = (flags & MLA_FLAG_Q_FP8) != 0;
-  if (q == nullptr || cache == nullptr || out == nullptr || workspace == nullptr) return MLA_ERR_INVALID_ARG;
+  if (q == nullptr || (cache == nullptr && num_blocks > 0) || out == nullptr || workspace == nullptr) return MLA_ERR_INVALID_ARG;
   if ((q8 && q_scale == nullptr) || (format == MLA_CACHE_E4M3 && kv_scale == nullptr)) return MLA_ERR_INVALID_ARG;
   if (G > 0 && (prefix_table == nullptr || prefix_lens == nullptr || prefix_cols < 1)) return MLA_ERR_INVALID_ARG;
   if (G > 1 && group_offsets == nullptr) return MLA_ERR_INVALID_ARG;

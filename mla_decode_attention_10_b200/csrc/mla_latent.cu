@@ -441,7 +441,8 @@ mla_status mla_latent_gather_launch(const void* cache, int32_t format, int64_t b
     return MLA_ERR_INVALID_ARG;
   if (num_blocks > (INT64_C(1) << 50) / block_size) return MLA_ERR_INVALID_ARG;
   if (B == 0 || N == 0) return MLA_OK;
-  if (cache == nullptr || block_table == nullptr || cu_rows == nullptr || out == nullptr) return MLA_ERR_INVALID_ARG;
+  if ((cache == nullptr && num_blocks > 0) || block_table == nullptr || cu_rows == nullptr || out == nullptr)
+    return MLA_ERR_INVALID_ARG;
   if (format == MLA_CACHE_E4M3 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
   if (N > 1 && out_stride < 576) return MLA_ERR_INVALID_ARG;
   if (!aligned(cache, 16) || !aligned(out, 16) || (N > 1 && out_stride % 8 != 0)) return MLA_ERR_ALIGNMENT;
