@@ -220,7 +220,9 @@ constexpr float kF8Top = 15.0f;
 // A score's scale and its difference to the reference are one rounding, but the
 // reference has been rounded too, by half a unit: that far the largest weight may
 // be from 1.  Where the unit passes 1, kF8 weights go without lift and margin; where
-// it would lead out of a weight's type, the row is NaN.
+// it would lead out of a weight's type, weights are zero while the maximum is there,
+// and a row whose maximum stays there is NaN: by its infinite reference, or, of low
+// scores, because it has a maximum but no denominator.
 constexpr float kF8Large = 4194304.0f;                       // 2^22
 constexpr float kF8Most = 268435456.0f;                       // 2^28: off by 2^8 at most
 constexpr float kMost = 2147483648.0f;                       // 2^31: by 2^64
@@ -1491,6 +1493,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
     const Segment seg = sh.segments[segs % kSegments];
     if (seg.k0 == seg.k1) break;
     segment_done(sh, segs);
+    constexpr float kMostOf = OP == kF8 ? kF8Most : kMost;
     const float lift = OP == kF8 ? f8_lift(seg.k1 - seg.k0) : 0.0f;
     float m = -INFINITY;      // the row's maximum when the reference last moved, in powers of two
     float ref = 0.0f;         // the reference
@@ -1564,8 +1567,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
             next_ref = large ? next : next - lift;
             limit = large ? next : next + (kF8Top - lift);
           }
-          if (fabsf(next) >= (OP == kF8 ? kF8Most : kMost)) next_ref = __uint_as_float(0x7fffffffu);
-          if (!first) factor = m == -INFINITY ? 0.0f : exp2_fast(ref - next_ref);
+          if (fabsf(next) >= kMostOf) next_ref = INFINITY;
+          if (!first) factor = m <= -kMostOf ? 0.0f : exp2_fast(ref - next_ref);
           m = next;
           ref = next_ref;
         }
@@ -1673,7 +1676,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared& sh, uint32
       float den = l;
 #pragma unroll
       for (int i = 1; i < kParts; ++i) den += sh.xch[i][r];
-      __stcg(stat + r, m == -INFINITY ? m : ref);
+      __stcg(stat + r, m <= -kMostOf ? m : ref);
       __stcg(stat + seg.part_rows + r, den);
     }
     bar_sync(bar_b, kShare);
@@ -2019,9 +2022,11 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const Params p, i
   den = 0.0f;
 #pragma unroll
   for (int i = 0; i < kJoinWorkers; ++i) den += red[1][i][row];
+  if (den == 0.0f && top > -INFINITY) den = __uint_as_float(0x7fffffffu);
+  const bool some = den > 0.0f || den != den;
   if (live && slice == 0 && wk == 0 && p.lse != nullptr)
-    p.lse[t * p.H + h] = den > 0.0f || den != den ? (ref + log2f(den)) * 0.6931471805599453f : -INFINITY;
-  float mul = den > 0.0f || den != den ? 1.0f / den : 0.0f;
+    p.lse[t * p.H + h] = some ? (ref + log2f(den)) * 0.6931471805599453f : -INFINITY;
+  float mul = some ? 1.0f / den : 0.0f;
   if (p.kv_scale != nullptr) mul *= __ldcg(p.kv_scale);
 
   // ---- sums
