@@ -300,9 +300,9 @@ MLA_API mla_status mla_latent_gather_launch(
  * statistics and partial sums are fp32; the softmax weights are rounded to bf16
  * before they multiply the keys.  When both q and the cache are e4m3, the codes
  * themselves are multiplied, and a weight is the sum of three e5m2 numbers (nine
- * bits, one more than bf16's; what weights too small for that lose is together at
- * most 2^-11 of the denominator, or 2^-30 for each key of a token where those are
- * more).  A product of q and a key beyond fp32's range is an
+ * bits, one more than bf16's; with scores below 2^21, what weights too small for
+ * that lose is together at most 2^-11 of the denominator, or 2^-30 for each key of a
+ * token where those are more).  A product of q and a key beyond fp32's range is an
  * infinity, and a row whose largest score is one comes out as NaN.  So may a row
  * whose largest score is beyond 2^30 in magnitude, or 2^27 with q and cache in e4m3.
  *
@@ -317,12 +317,12 @@ MLA_API mla_status mla_latent_gather_launch(
  *           table_cols == 0 (block_table NULL): no token has keys of its own
  *   out     bf16 [T, H, 512] contiguous, 16-byte aligned;  lse fp32 [T, H] or NULL
  *   workspace  mla_prefix_attend_workspace_for() bytes (prefix_keys = prefix_cols *
- *           block_size; sm_count 0: of the current device) of device memory;
- *           mla_prefix_attend_workspace() bytes are enough for every cache.  Large
- *           groups over rows that need decoding take 73856 bytes for each 64 keys of
- *           prefix_keys, up to 2 GiB, the others none;
- *           256-byte aligned; need not be initialised, holds nothing between calls;
- *           two calls that may run at the same time need two
+ *           block_size; sm_count 0: of the current device) of device memory, 256-byte
+ *           aligned; mla_prefix_attend_workspace() bytes are enough for every cache.
+ *           Groups of 256 rows or more on average, over a cache that needs decoding or
+ *           has odd pages, take up to 73856 bytes for each 64 keys of prefix_keys, 2 GiB
+ *           at most.  Need not be initialised, holds nothing between calls; two calls
+ *           that may run at the same time need two
  *   flags   MLA_FLAG_Q_FP8, MLA_FLAG_PDL (everything is read after the wait)
  * A negative length counts as 0.  A length beyond its table is cut to it and sets
  * MLA_STATUS_LEN_RANGE.  Keys in a page outside [0, num_blocks) are left out and

@@ -132,7 +132,11 @@ def mla_latent_cache_insert(
     ``kv_c`` bf16 [T, 512] and ``k_pe`` bf16 [T, 64] (inner stride 1),
     ``slot_mapping`` int64 [T] (negative: no row).  With ``norm_weight`` (bf16
     [512]) the latents are RMS-normalised first; with ``cos_sin`` (fp32 [rows,
-    64]) and ``positions`` (int32 [T]) the rotary values are rotated.
+    64]) and ``positions`` (int32 [T]) the rotary values are rotated.  With
+    ``pdl`` the previous kernel on the stream may write ``kv_c`` and ``k_pe``
+    only: everything else is read while it may still be running.  A step that
+    takes its query rows from the epilogue gives that a cache without pages
+    (``torch.empty((0, block, 576))``) and slots of -1, in a call of its own.
     """
     index, fmt, scale = _cache(cache, kv_scale)
     T = kv_c.shape[0]
@@ -165,6 +169,7 @@ def mla_latent_cache_gather(
     land in ``out[cu_rows[b]:cu_rows[b+1]]``; ``block_table`` is int32 [B,
     pages], ``cu_rows`` int32 [B + 1], ascending.  Rows of ``out`` that belong
     to no sequence stay as they were (uninitialised in an ``out`` made here).
+    With ``pdl`` everything is read after the previous kernel on the stream.
     """
     index, fmt, scale = _cache(cache, kv_scale)
     table, table_stride, cols = _table("block_table", block_table, index, -1)
@@ -218,9 +223,16 @@ def mla_prefix_decode_attention(
     tokens ``group_offsets[g] .. group_offsets[g + 1] - 1`` (int32 [G + 1]; None
     with one group: every token).  Without ``prefix_table`` there are no
     prefixes.  A ``workspace`` (uint8, at least ``mla_prefix_attend_workspace_for``
-    bytes, or ``mla_prefix_attend_workspace`` for any cache) must not be shared by calls that may run at the same time; without
-    one each call takes its own.  Rows whose computation a timeout cut short
-    (``MLA_STATUS_TIMEOUT`` in ``status``) are NaN.
+    bytes, or ``mla_prefix_attend_workspace`` for any cache) must not be shared by
+    calls that may run at the same time; without one each call takes its own.
+    Rows whose computation a timeout cut short (``MLA_STATUS_TIMEOUT`` in
+    ``status``) are NaN.
+
+    Where the cache needs decoding (or has odd pages) and groups have 256 rows
+    (token, head) or more on average, the workspace has room for all of
+    ``prefix_table``'s width, up to 73856 bytes for 64 keys; beyond 2 GiB there is
+    none, and prefixes are decoded once for each 64 rows, which takes up to 1.8
+    times as long.  So a table is best no wider than its longest prefix.
     """
     index, fmt, scale = _cache(cache, kv_scale)
     if q.dim() != 3:
