@@ -66,11 +66,11 @@ KERNEL_SOURCES = ("mla_decode_attention_10_b200/csrc/mla_epilogue.cu",
                   "mla_decode_attention_10_b200/csrc/mla_rows.cu",
                   "mla_decode_attention_10_b200/csrc/epilogue_device.cuh",
                   "mla_decode_attention_10_b200/csrc/latent_math.cuh", "include/mla_epilogue.h")
-TRAFFIC_SOURCE_HASH = "e2925e738a49936e"
+TRAFFIC_SOURCE_HASH = "fc63cc6517c5dd0d"
 TRAFFIC_BYTES = {
-    "batch_t8192_h16_pdl_fp8": 163967744 + 49781248,
+    "batch_t8192_h16_pdl_fp8": 163968000 + 50129920,
     "split_boundary_t64_h16_rope": 1279488 + 0,
-    "prefill_t1024_h128_strided": 152637440 + 100397312,
+    "prefill_t1024_h128_strided": 152630528 + 101770752,
 }
 L2_BYTES = 126 * 2 ** 20
 # The weight-streaming producer (decode sizes): the weights a projection
